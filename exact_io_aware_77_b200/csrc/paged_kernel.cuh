@@ -273,10 +273,11 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
     tma_prefetch_desc(&tm_v);
   }
   __syncwarp();
-  // this grid may be scheduled while the one before it runs (which may be writing the cache or the
-  // lengths, or still read this scratch); with a shared prefix the one before is the prefix's, which
-  // started after all that and writes nothing read here, so only this grid's end waits for it
-  if (!p.o_row) grid_dep_wait();
+  // This grid may be scheduled while the one before it runs.  Nothing that another grid may have written
+  // (lengths, tables, q, pages) is read before the wait, and the scratch is not written: that a grid
+  // earlier on the stream has ended makes its writes visible only to the grids that waited for it, and
+  // with a shared prefix this one waits for the prefix's.
+  grid_dep_wait();
   // ---- the line of work: every warp adds up the lengths (lane l a run of `per` sequences)
   const int HR = p.H_kv * p.row_blocks;
   const int per = (p.B + 31) >> 5;
@@ -297,10 +298,7 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
   const int run_end = pg_warp_scan(mine, lane), run_at = run_end - mine;
   const int all = __shfl_sync(0xffffffffu, run_end, 31);
   const PgCut cut(all * HR, p.warps, pg_parts(D));
-  if (int(blockIdx.x) >= cut.n) {
-    grid_dep_wait();   // see the end of the kernel
-    return;
-  }
+  if (int(blockIdx.x) >= cut.n) return;
   ask();
   int asked = 1;   // requests made
   bool open = true, dry = false;   // the last one is not answered yet; there is no further piece
@@ -749,10 +747,6 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
   if (lane == 0)
     for (int j = it; j < issued; ++j)
       mbar_wait_drain(smem_u32(&bars[j % kPgStages]), (j / kPgStages) & 1, p.wait_limit_ns);
-  __syncwarp();
-  // with a shared prefix the grid before this one (its splits) may still be running: this grid
-  // ends after it, so that the merge, which waits for this one, finds both complete
-  grid_dep_wait();
 }
 
 __device__ __forceinline__ float* merge_smem() { return reinterpret_cast<float*>(dec_dyn_smem()); }
@@ -774,7 +768,10 @@ __global__ void __launch_bounds__(32 * kPgMergeWarps) fa_paged_merge_kernel(cons
   const int b = bh / p.H, hq = bh - b * p.H;
   const int hkv = hq / p.group, r = (hq - hkv * p.group) * p.Nq + i;
   const int HR = p.H_kv * p.row_blocks;
-  // the row's item on the line, from the lengths alone: known before the grid before has ended
+  // not even the lengths are read before the wait: the grid before this one has seen them, which
+  // makes them visible to that grid alone
+  grid_dep_wait();
+  // the row's item on the line, from the lengths alone
   int before = 0, all = 0;
   for (int x = lane; x < p.B; x += 32) {
     const int u = pg_units<kStep>(p, x);
@@ -792,7 +789,6 @@ __global__ void __launch_bounds__(32 * kPgMergeWarps) fa_paged_merge_kernel(cons
   const int c1 = steps > 0 ? cut.of(s + n - 1) : c_item;
   const bool whole = c0 == c1;
   const int n_own = whole ? 1 : c1 - c0 + 1, n_src = n_own + p.n_pre;
-  grid_dep_wait();
   if (whole && !p.o_row) return;
   // the prefix's rows of one K/V head: those of all sequences, in order
   const long long pre_row = ((long long)hkv * p.B + b) * p.rows + r;

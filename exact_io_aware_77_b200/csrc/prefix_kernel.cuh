@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(pf_threads(kFp8), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<const volatile uint32_t*>(smem + Sm::kTmemBase);
-  // the grid before this one has ended (q's producer, the append); the next one, the own keys', reads
-  // nothing of this one's and may start
+  // the grid before this one has ended (q's producer, the append); the next one, the own keys', may be
+  // scheduled and waits for this one in its turn
   grid_dep_wait();
   grid_dep_launch_dependents();
 

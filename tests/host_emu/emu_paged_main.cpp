@@ -30,6 +30,36 @@ void write_file(const std::string& path, const std::vector<T>& v) {
   f.write(reinterpret_cast<const char*>(v.data()), v.size() * sizeof(T));
 }
 
+// With "hidden" in front of the arguments: before every grid, what other grids or the host have written
+// is replaced by other values, and comes back when a thread of the grid waits for the grids before.
+struct Hidden {
+  unsigned char* at;
+  std::vector<unsigned char> kept;
+  int fill;
+};
+static bool hide_inputs = false;
+static std::vector<Hidden> hidden;
+static bool is_hidden = false;
+static std::mutex hidden_mu;
+template <class T>
+static void hideable(std::vector<T>& v, int fill) {
+  if (!v.empty()) hidden.push_back(Hidden{reinterpret_cast<unsigned char*>(v.data()), std::vector<unsigned char>(v.size() * sizeof(T)), fill});
+}
+static void hide() {
+  if (!hide_inputs) return;
+  for (Hidden& h : hidden) {
+    std::copy(h.at, h.at + h.kept.size(), h.kept.begin());
+    std::memset(h.at, h.fill, h.kept.size());
+  }
+  is_hidden = true;
+  emu_on_dep_wait = [] {
+    std::lock_guard<std::mutex> lk(hidden_mu);
+    if (!is_hidden) return;
+    for (Hidden& h : hidden) std::copy(h.kept.begin(), h.kept.end(), h.at);
+    is_hidden = false;
+  };
+}
+
 static char** arg;
 static int num() { return atoi(*arg++); }
 static float fnum() { return float(atof(*arg++)); }
@@ -62,11 +92,14 @@ void run_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& 
   if (x) {
     CUtensorMap pk = tk, pv = tv;
     pk.box_rows = pv.box_rows = uint32_t(x->box_rows);
+    hide();
     emu_launch(unsigned(x->H_kv * x->n_splits * x->row_groups), pf_threads(kFp8), PrefixSmem<D, kFp8>::kAlloc,
                [&] { fa_prefix_kernel<D, kFp8>(q_map(*x, D), pk, pv, *x); }, dec_smem);
   }
+  hide();
   emu_launch(unsigned(p.warps) * pg_parts(D), 32, PgLayout<D, kFp8>::kSmemBytes,
              [&] { fa_paged_kernel<D, kFp8>(tk, tv, p); }, dec_smem);
+  hide();
   // four warps a row, or one when there are many rows
   emu_launch(unsigned(p.total_rows), p.total_rows <= 48 ? 32 * kPgMergeWarps : 32, pg_merge_smem(D),
              [&] { fa_paged_merge_kernel<D, PgLayout<D, kFp8>::kStep>(p); }, dec_smem);
@@ -155,6 +188,13 @@ static int paged_main(bool shared) {
     p.o_pre = x.o_pre = o_pre.data();
     p.l_pre = x.l_pre = l_pre.data();
   }
+  hideable(q, 0x7f);
+  hideable(k, 0);
+  hideable(v, 0);
+  hideable(table, 0);
+  hideable(lengths, 0);
+  for (auto* part : {&o_part, &l_part, &o_row, &l_row, &o_pre, &l_pre}) hideable(*part, 0xff);
+  if (shared) hideable(pages, 0);
   const PrefixParams* xp = shared ? &x : nullptr;
   if (d == 64) fp8 ? run_paged<64, true>(tk, tv, p, xp) : run_paged<64, false>(tk, tv, p, xp);
   else if (d == 128) fp8 ? run_paged<128, true>(tk, tv, p, xp) : run_paged<128, false>(tk, tv, p, xp);
@@ -242,7 +282,9 @@ static int append_main() {
 
 int main(int argc, char** argv) {
   if (argc < 2) return 2;
-  const std::string what = argv[1];
-  arg = argv + 2;
+  hide_inputs = std::string(argv[1]) == "hidden";
+  arg = argv + (hide_inputs ? 3 : 2);
+  if (arg > argv + argc) return 2;
+  const std::string what = arg[-1];
   return what == "append" ? append_main() : paged_main(what == "shared");
 }

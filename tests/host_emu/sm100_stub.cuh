@@ -101,8 +101,12 @@ inline uint32_t bf16x2_to_f16x2_sat(uint32_t w) {
   return pack_f16x2(lo, hi);
 }
 inline unsigned char* dec_dyn_smem() { return g_blk->smem; }
-// programmatic dependent launch: the emulation runs grids one after another, so both are no-ops
-inline void grid_dep_wait() {}
+// programmatic dependent launch: the emulation runs grids one after another, so both are no-ops, but
+// that a harness may let its inputs appear only with the wait
+inline std::function<void()> emu_on_dep_wait;
+inline void grid_dep_wait() {
+  if (emu_on_dep_wait) emu_on_dep_wait();
+}
 inline void grid_dep_launch_dependents() {}
 
 // cta_steal_async takes the grid's next CTA out of emu_launch's hands; the answer is written when
