@@ -465,7 +465,8 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
       }
     }
     fence_proxy_async_smem();   // the stage is next written by TMA
-    return __any_sync(0xffffffffu, bad);   // and every lane has cleared its part
+    __syncwarp();               // other lanes read what this one has cleared (a vote orders no memory)
+    return __any_sync(0xffffffffu, bad);
   };
 
   int it = 0;              // my steps done

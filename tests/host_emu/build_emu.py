@@ -47,7 +47,8 @@ PATCHES = {
 
 
 def build(out_dir: str, kernel_header, harness: str, exe_name: str, defines=()) -> str:
-    """kernel_header: one header name, or a list (a kernel header and the headers it includes)."""
+    """kernel_header: one header name, or a list (a kernel header and the headers it includes).  With
+    EMU_UNORDERED among the defines the binary is built for ThreadSanitizer."""
     headers = [kernel_header] if isinstance(kernel_header, str) else list(kernel_header)
     # and every library header they include (sm100.cuh and the stubbed headers are the stub's)
     i = 0
@@ -82,7 +83,8 @@ def build(out_dir: str, kernel_header, harness: str, exe_name: str, defines=()) 
     shutil.copy(os.path.join(HERE, "emu.h"), os.path.join(out_dir, "emu.h"))
     shutil.copy(os.path.join(HERE, harness), os.path.join(out_dir, harness))
     exe = os.path.join(out_dir, exe_name)
-    cmd = [gxx, "-std=c++20", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+    sanitize = "thread" if "EMU_UNORDERED" in defines else "address,undefined"
+    cmd = [gxx, "-std=c++20", "-O1", "-g", f"-fsanitize={sanitize}", "-fno-sanitize-recover=all",
            "-fno-omit-frame-pointer", "-pthread"] + [f"-D{d}" for d in defines] + \
           ["-x", "c++", os.path.join(out_dir, harness), "-o", exe]
     r = subprocess.run(cmd, capture_output=True, text=True)

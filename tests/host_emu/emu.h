@@ -57,10 +57,38 @@ inline uint32_t __float_as_uint(float f) {
 inline int atomicOr(int* p, int v) { return __atomic_fetch_or(p, v, __ATOMIC_SEQ_CST); }
 struct __nv_bfloat16 { uint16_t x; };
 
+// Shuffles, votes, matrix loads and warp MMAs meet in lockstep but, as on the device, order no
+// memory: built with EMU_UNORDERED (for ThreadSanitizer) their lanes meet and exchange through
+// relaxed atomics alone, so that only __syncwarp and __syncthreads order what lanes store and load.
+template <class T>
+struct Exchanged {
+#ifdef EMU_UNORDERED
+  std::atomic<T> v;
+  operator T() const { return v.load(std::memory_order_relaxed); }
+  void operator=(T x) { v.store(x, std::memory_order_relaxed); }
+#else
+  T v;
+  operator T() const { return v; }
+  void operator=(T x) { v = x; }
+#endif
+};
 struct WarpCtx {
   std::barrier<>* bar;
-  uint32_t xch[32][12];
-  const void* addr[32];
+  Exchanged<uint32_t> xch[32][12];
+  Exchanged<const void*> addr[32];
+#ifdef EMU_UNORDERED
+  std::atomic<unsigned> met{0};
+  WarpCtx() = default;
+  WarpCtx(const WarpCtx&) {}
+#endif
+  void meet() {
+#ifdef EMU_UNORDERED
+    const unsigned until = met.fetch_add(1, std::memory_order_relaxed) / 32 * 32 + 32;
+    while (int(met.load(std::memory_order_relaxed) - until) < 0) std::this_thread::yield();
+#else
+    bar->arrive_and_wait();
+#endif
+  }
 };
 // mbarrier state, kept beside shared memory (keyed by the barrier's shared-memory offset)
 struct BarState {
@@ -91,11 +119,10 @@ inline void __syncwarp(unsigned = 0xffffffffu) { my_warp().bar->arrive_and_wait(
 inline float __shfl_xor_sync(unsigned, float v, int m) {
   WarpCtx& w = my_warp();
   int l = lane_id();
-  std::memcpy(&w.xch[l][0], &v, 4);
-  w.bar->arrive_and_wait();
-  float r;
-  std::memcpy(&r, &w.xch[l ^ m][0], 4);
-  w.bar->arrive_and_wait();
+  w.xch[l][0] = __float_as_uint(v);
+  w.meet();
+  const float r = __uint_as_float(w.xch[l ^ m][0]);
+  w.meet();
   return r;
 }
 
@@ -108,30 +135,29 @@ inline int __all_sync(unsigned, int pred) {
   WarpCtx& w = my_warp();
   int l = lane_id();
   w.xch[l][0] = pred ? 1u : 0u;
-  w.bar->arrive_and_wait();
+  w.meet();
   int all = 1;
   for (int i = 0; i < 32; ++i) all &= int(w.xch[i][0]);
-  w.bar->arrive_and_wait();
+  w.meet();
   return all;
 }
 inline int __any_sync(unsigned, int pred) {
   WarpCtx& w = my_warp();
   int l = lane_id();
   w.xch[l][0] = pred ? 1u : 0u;
-  w.bar->arrive_and_wait();
+  w.meet();
   int any = 0;
   for (int i = 0; i < 32; ++i) any |= int(w.xch[i][0]);
-  w.bar->arrive_and_wait();
+  w.meet();
   return any;
 }
 inline float __shfl_sync(unsigned, float v, int src) {
   WarpCtx& w = my_warp();
   int l = lane_id();
-  std::memcpy(&w.xch[l][0], &v, 4);
-  w.bar->arrive_and_wait();
-  float r;
-  std::memcpy(&r, &w.xch[src & 31][0], 4);
-  w.bar->arrive_and_wait();
+  w.xch[l][0] = __float_as_uint(v);
+  w.meet();
+  const float r = __uint_as_float(w.xch[src & 31][0]);
+  w.meet();
   return r;
 }
 inline int __shfl_sync(unsigned mask, int v, int src) {
@@ -152,19 +178,19 @@ inline int __shfl_xor_sync(unsigned mask, int v, int m) {
 inline unsigned __ballot_sync(unsigned, int pred) {
   WarpCtx& w = my_warp();
   w.xch[lane_id()][0] = pred ? 1u : 0u;
-  w.bar->arrive_and_wait();
+  w.meet();
   unsigned all = 0;
   for (int i = 0; i < 32; ++i) all |= w.xch[i][0] << i;
-  w.bar->arrive_and_wait();
+  w.meet();
   return all;
 }
 inline int __shfl_up_sync(unsigned, int v, int delta) {
   WarpCtx& w = my_warp();
   const int l = lane_id();
   w.xch[l][0] = uint32_t(v);
-  w.bar->arrive_and_wait();
+  w.meet();
   const int r = int(w.xch[l < delta ? l : l - delta][0]);
-  w.bar->arrive_and_wait();
+  w.meet();
   return r;
 }
 

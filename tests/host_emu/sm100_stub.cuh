@@ -141,28 +141,28 @@ inline void ldmatrix_x4(uint32_t (&r)[4], const void* row) {
   WarpCtx& w = my_warp();
   int l = lane_id();
   w.addr[l] = row;
-  w.bar->arrive_and_wait();
+  w.meet();
   for (int m = 0; m < 4; ++m) {
-    const unsigned char* a = static_cast<const unsigned char*>(w.addr[m * 8 + l / 4]);
+    const unsigned char* a = static_cast<const unsigned char*>(static_cast<const void*>(w.addr[m * 8 + l / 4]));
     std::memcpy(&r[m], a + 4 * (l % 4), 4);
   }
-  w.bar->arrive_and_wait();
+  w.meet();
 }
 inline void ldmatrix_x4_trans(uint32_t (&r)[4], const void* row) {
   check_row_addr(row);
   WarpCtx& w = my_warp();
   int l = lane_id();
   w.addr[l] = row;
-  w.bar->arrive_and_wait();
+  w.meet();
   for (int m = 0; m < 4; ++m) {
-    const unsigned char* r0 = static_cast<const unsigned char*>(w.addr[m * 8 + 2 * (l % 4)]);
-    const unsigned char* r1 = static_cast<const unsigned char*>(w.addr[m * 8 + 2 * (l % 4) + 1]);
+    const unsigned char* r0 = static_cast<const unsigned char*>(static_cast<const void*>(w.addr[m * 8 + 2 * (l % 4)]));
+    const unsigned char* r1 = static_cast<const unsigned char*>(static_cast<const void*>(w.addr[m * 8 + 2 * (l % 4) + 1]));
     uint16_t lo, hi;
     std::memcpy(&lo, r0 + 2 * (l / 4), 2);
     std::memcpy(&hi, r1 + 2 * (l / 4), 2);
     r[m] = uint32_t(lo) | (uint32_t(hi) << 16);
   }
-  w.bar->arrive_and_wait();
+  w.meet();
 }
 template <class Dec>
 inline void mma_emu(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, Dec dec) {
@@ -171,12 +171,12 @@ inline void mma_emu(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
   for (int i = 0; i < 4; ++i) w.xch[l][i] = a[i];
   w.xch[l][4] = b0;
   w.xch[l][5] = b1;
-  for (int i = 0; i < 4; ++i) std::memcpy(&w.xch[l][6 + i], &d[i], 4);
-  w.bar->arrive_and_wait();
+  for (int i = 0; i < 4; ++i) w.xch[l][6 + i] = __float_as_uint(d[i]);
+  w.meet();
   float A[16][16], B[16][8], C[16][8];
   for (int L = 0; L < 32; ++L) {
     const int g = L >> 2, t = L & 3;
-    const uint32_t* x = w.xch[L];
+    const auto& x = w.xch[L];
     auto lo = [&](uint32_t v) { return dec(uint16_t(v & 0xffff)); };
     auto hi = [&](uint32_t v) { return dec(uint16_t(v >> 16)); };
     A[g][2 * t] = lo(x[0]); A[g][2 * t + 1] = hi(x[0]);
@@ -185,10 +185,8 @@ inline void mma_emu(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
     A[g + 8][2 * t + 8] = lo(x[3]); A[g + 8][2 * t + 9] = hi(x[3]);
     B[2 * t][g] = lo(x[4]); B[2 * t + 1][g] = hi(x[4]);
     B[2 * t + 8][g] = lo(x[5]); B[2 * t + 9][g] = hi(x[5]);
-    float c[4];
-    std::memcpy(c, &x[6], 16);
-    C[g][2 * t] = c[0]; C[g][2 * t + 1] = c[1];
-    C[g + 8][2 * t] = c[2]; C[g + 8][2 * t + 1] = c[3];
+    C[g][2 * t] = __uint_as_float(x[6]); C[g][2 * t + 1] = __uint_as_float(x[7]);
+    C[g + 8][2 * t] = __uint_as_float(x[8]); C[g + 8][2 * t + 1] = __uint_as_float(x[9]);
   }
   const int g = l >> 2, t = l & 3;
   const int rr[4] = {g, g, g + 8, g + 8}, cc[4] = {2 * t, 2 * t + 1, 2 * t, 2 * t + 1};
@@ -197,7 +195,7 @@ inline void mma_emu(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
     for (int k = 0; k < 16; ++k) s += A[rr[i]][k] * B[k][cc[i]];
     d[i] = s;
   }
-  w.bar->arrive_and_wait();
+  w.meet();
 }
 inline void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   mma_emu(d, a, b0, b1, [](uint16_t h) { return bf2f(h); });

@@ -6,7 +6,20 @@ import pytest
 import torch
 
 from tests import paged_ref as ref
-from tests.test_paged_emulated import _bf16, _run, _strides, exes  # noqa: F401
+from tests.test_paged_emulated import _bf16, _run, _strides
+
+
+@pytest.fixture(scope="module")
+def exes(tmp_path_factory):
+    """late: as in test_paged_emulated.py; unordered: under ThreadSanitizer, with warps whose votes,
+    shuffles, matrix loads and MMAs order no memory."""
+    from tests.host_emu.build_emu import build_many
+    try:
+        return build_many(str(tmp_path_factory.mktemp("paged_edges")), {
+            "late": ("prefix_kernel.cuh", "emu_paged_main.cpp", "emu_paged", ()),
+            "unordered": ("prefix_kernel.cuh", "emu_paged_main.cpp", "emu_paged_tsan", ("EMU_UNORDERED",))})
+    except FileNotFoundError:
+        pytest.skip("g++ not available")
 
 
 def _paged(exe, pre, q, k, v, table, lengths, H_kv, causal=True, window=0, fp8=False, ctas=3, prefix=None, hidden=False,
@@ -28,7 +41,7 @@ def _paged(exe, pre, q, k, v, table, lengths, H_kv, causal=True, window=0, fp8=F
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("shared", [False, True])
-def test_nothing_is_read_before_the_wait(exes, tmp_path, shared, fp8):  # noqa: F811
+def test_nothing_is_read_before_the_wait(exes, tmp_path, shared, fp8):
     """Every grid may be scheduled while the one before it runs, and sees what other grids have written
     (lengths, tables, queries, pages, partial results) only once it has waited for it."""
     gen = ref.rng(51)
@@ -42,3 +55,15 @@ def test_nothing_is_read_before_the_wait(exes, tmp_path, shared, fp8):  # noqa: 
     ks, vs = (0.0125, 0.01) if fp8 else (1.0, 1.0)
     ref.assert_attention(o, lse, ref.attention(q, k, v, table, lengths, d ** -0.5, True, 0, ks, vs,
                                                prefix=(pages.tolist(), prefix) if shared else None))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_lanes_meet_before_they_read_cleared_rows(exes, tmp_path, fp8):
+    """V rows behind the mask are cleared by some lanes and read by others: no data race (a race
+    makes the binary's exit status 66)."""
+    gen = ref.rng(12)
+    lengths, N_q, window = [21, 0, 50, 5], 3, 30
+    k, v, table, q, want, hit = ref.poisoned(gen, lengths, N_q, window, 16, fp8)
+    o, lse, status = _paged(exes["unordered"], str(tmp_path / "x"), q, k, v, table, lengths, 2, window=window, fp8=fp8)
+    assert status == 0
+    ref.assert_poisoned(o, lse, want, hit)
