@@ -497,6 +497,9 @@ int check_cache(const fa_paged_kv* c, int H_kv, int d, Strides* ks, Strides* vs)
   return FA_OK;
 }
 
+// a factor that the kernels form from the caller's scales: neither gone to 0 nor past fp32's range
+bool usable_factor(float x) { return std::isfinite(x) && x > 0.f; }
+
 // programmatic dependent launch: the grid may be scheduled before the previous one on the stream has
 // ended, and waits for its results in the kernel (grid_dep_wait)
 template <class... Params, class... Args>
@@ -625,6 +628,11 @@ int launch_paged(const PagedParams& p, const fa_paged_kv& c, const Strides& ks, 
                           pg_merge_smem(D), stream, p);
 }
 
+// of a score's exponent in base 2: scale, the codes' scale and log2 e
+float score_factor(float scale, const fa_paged_kv& c) {
+  return scale * (c.fp8 ? c.k_scale : 1.f) * 1.4426950408889634f;
+}
+
 // Everything but the prefix's and whole rows' places.
 PagedParams paged_params(const void* q, const fa_paged_kv& c, const int* lengths, void* o, float* lse, int B, int H,
                          int H_kv, int Nq, int d, const Strides& qs, const Strides& os, float scale, int causal,
@@ -657,7 +665,7 @@ PagedParams paged_params(const void* q, const fa_paged_kv& c, const int* lengths
   p.window = window;
   p.part_rows = p.rows < kDecRows ? p.rows : kDecRows;
   p.warps = pg_warps(d, c.fp8);
-  p.scale_log2 = scale * (c.fp8 ? c.k_scale : 1.f) * 1.4426950408889634f;
+  p.scale_log2 = score_factor(scale, c);
   p.v_scale = c.v_scale;
   p.wait_limit_ns = g_wait_limit_ns;
   return p;
@@ -1052,6 +1060,9 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, const
     p.n_angles = r.n_angles;
     p.axes = r.axes;
   }
+  p.k_inv = cache->fp8 ? 1.f / cache->k_scale : 1.f;
+  p.v_inv = cache->fp8 ? 1.f / cache->v_scale : 1.f;
+  if (!usable_factor(p.k_inv) || !usable_factor(p.v_inv)) return FA_ERR_SCALE;
   if ((st = check_device()) != FA_OK) return st;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
@@ -1075,8 +1086,6 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, const
   p.n_pages = cache->n_pages;
   p.page_size = cache->page_size;
   p.max_pages = cache->max_pages;
-  p.k_inv = cache->fp8 ? 1.f / cache->k_scale : 1.f;
-  p.v_inv = cache->fp8 ? 1.f / cache->v_scale : 1.f;
   const bool inter = rotation && rotation->interleaved;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (d) {
@@ -1125,7 +1134,7 @@ static int paged_impl(const void* q, const fa_paged_kv* cache, const int* prefix
   Strides ks, vs, qs, os;
   if (st == FA_OK) st = check_cache(cache, H_kv, d, &ks, &vs);
   if (st != FA_OK) return st;
-  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_SCALE;
+  if (!std::isfinite(scale) || !(scale > 0.f) || !usable_factor(score_factor(scale, *cache))) return FA_ERR_SCALE;
   if ((st = row_strides(strides, B, H, N_q, d, &qs, &os)) != FA_OK) return st;
   const int rows = H / H_kv * N_q;
   const long long R = (long long)B * rows, total = R * H_kv;

@@ -250,6 +250,8 @@ FA_EXPORT int fa_fwd_fp8(const void* q8, const void* k8, const void* vt8, float 
  *   table       device int32 [B, max_pages], rows table_stride >= max_pages apart.  Only the
  *               entries that the lengths reach are read.
  *   page_size   a multiple of 16, at most 32768.
+ *   k_scale, v_scale   finite and > 0, and so must be what the kernels form of them in fp32 (FA_ERR_SCALE):
+ *               1 / k_scale and 1 / v_scale in the append, scale * k_scale * log2(e) in the forwards.
  *
  * Page numbers, lengths and positions live on the device, so that a captured graph follows a growing
  * cache.  One that is out of range is never used as an address: what it would place or turn is not

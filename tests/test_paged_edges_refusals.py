@@ -1,0 +1,25 @@
+"""More calls of the paged cache that are refused on the host (no GPU needed: addresses are made up, and
+validation must end before any use)."""
+
+import pytest
+
+from exact_io_aware_77_b200 import _lib
+from tests.test_paged_refusals import _append, _cache, _name, _paged, _shared, lib  # noqa: F401
+
+
+@pytest.mark.parametrize("call", [_paged, _shared], ids=["paged", "shared"])
+@pytest.mark.parametrize("scale,k_scale", [(1e-30, 1e-20), (1e30, 1e20), (1e38, 3.0)])
+def test_score_factors_out_of_range_are_refused(lib, call, scale, k_scale):  # noqa: F811
+    """scale * k_scale gone to 0 or past fp32's range: every score would be NaN."""
+    assert _name(call(cache=_cache(fp8=1, k_scale=k_scale), scale=scale)) == "FA_ERR_SCALE"
+
+
+@pytest.mark.parametrize("call", [_paged, _shared], ids=["paged", "shared"])
+def test_scales_past_the_exponentials_base_are_refused(lib, call):  # noqa: F811
+    assert _name(call(scale=3e38)) == "FA_ERR_SCALE"     # scale * log2(e) is past fp32's range
+
+
+@pytest.mark.parametrize("kw", [dict(k_scale=1e-39), dict(v_scale=1e-39)])
+def test_scales_without_an_inverse_are_refused(lib, kw):  # noqa: F811
+    """1 / scale past fp32's range: zeros would become NaN codes."""
+    assert _name(_append(cache=_cache(fp8=1, **kw))) == "FA_ERR_SCALE"
