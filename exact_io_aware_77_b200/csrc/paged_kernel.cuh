@@ -53,6 +53,12 @@ constexpr int kPgStages = 3;
 constexpr int kPgSurcharge = 2;    // units a new item costs a warp before its first step (Q, output)
 constexpr int kPgMinPiece = 4;     // shortest piece of the line, in units
 constexpr int kPgMaxWarps = 148 * 8;
+// Over E4M3 pages the weights enter P V as f16.  They are formed 2^15 times as large, below f16's largest
+// value, so that a weight keeps f16's 11 bits down to 2^-29 of the row's largest (which the row's sum, in fp32,
+// counts in full) and is lost below 2^-40 only; formed as they are, keys 17.3 below the largest score would
+// be.  The difference to the largest score is formed first, so that no weight passes 2^15, however large
+// the scores.
+constexpr float kPgLift = 15.f;
 constexpr int kPgMergeWarps = 4;   // of one row, at most
 
 // 16-key blocks per step: as many as fill a stage of kPgStageBytes, up to four.  (With 16 KB stages and
@@ -612,7 +618,9 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
         for (int n = 0; n < 2 * kBlocks; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[n][2 * hf + e] = ex2_approx(s[n][2 * hf + e] * p.scale_log2 + m_use);
+            const float x = s[n][2 * hf + e];
+            s[n][2 * hf + e] =
+                ex2_approx(kFp8 ? (x - m_fin) * p.scale_log2 + kPgLift : x * p.scale_log2 + m_use);
             sum += s[n][2 * hf + e];
           }
         l_run[hf] = l_run[hf] * alpha[hf] + sum;   // this lane's share; summed over the group at the end
@@ -703,7 +711,8 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
       // a row without keys, or whose every key scored -inf, has l = 0; one with a NaN score is NaN
       float inv = l == 0.f ? 0.f : 1.f / l;
       if constexpr (kFp8) inv *= p.v_scale;
-      const float lse = l == 0.f ? -INFINITY : (m_run[hf] * p.scale_log2 + lg2_approx(l)) * kLn2;
+      const float lse =
+          l == 0.f ? -INFINITY : (m_run[hf] * p.scale_log2 + (lg2_approx(l) - (kFp8 ? kPgLift : 0.f))) * kLn2;
       const long long grow = ((long long)b * p.H + hq[hf]) * p.Nq + qi[hf];
       if (whole && !p.o_row) {
         __nv_bfloat16* dst = p.o + p.o_st.at(b, hq[hf], qi[hf]);

@@ -21,7 +21,7 @@
 //   warp 9       MMA issue: S = Q K^T into TMEM, O += P V with P from TMEM.
 //   warps 0-7    softmax: thread t of a stream owns row t (TMEM lane t): running max and sum, P packed
 //                to 16 bits over the S columns, O rescaled only when a row's max grows by more than
-//                2^8, and at the end O / l and L.
+//                2^8 (E4M3 pages: 2^4), and at the end O / l and L.
 //   warps 10-13  (E4M3 pages; at d = 256 warps 4-7 too: 73.5 us instead of 77.6 for 16 heads of 68 rows over
 //                10140 keys) convert each tile's codes, which TMA leaves in a ring of their own, to f16
 //                operand tiles; Q is rounded to f16 after clamping to its range, P is f16.
@@ -48,6 +48,13 @@ namespace fa {
 constexpr int kPfSlots = 4;
 constexpr int kPfRaw = 2;
 constexpr int kPfWarpTma = 8, kPfWarpMma = 9;
+// O is rescaled when a row's maximum has grown by more than 2^this since it was last.  Over E4M3 pages, whose
+// weights enter P V as f16, they are formed 2^kPfLift times as large (see kPgLift): those of a maximum that
+// has grown unseen stay below f16's largest value, and weights keep f16's 11 bits down to 2^-25 of the row's
+// largest and are lost below 2^-36 only.
+__host__ __device__ constexpr float pf_growth(bool fp8) { return fp8 ? 4.f : kRescaleThreshold; }
+constexpr float kPfLift = 11.f;
+static_assert(pf_growth(true) + kPfLift <= 15.f, "weights within f16");
 __host__ __device__ constexpr int pf_streams(int d) { return d == 256 ? 1 : 2; }
 __host__ __device__ constexpr int pf_keys(int d) { return d == 256 ? 64 : 128; }   // keys per tile
 __host__ __device__ constexpr int pf_threads(bool fp8) { return fp8 ? 448 : 320; }
@@ -483,19 +490,21 @@ __global__ void __launch_bounds__(pf_threads(kFp8), 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) mx16[i] = fmaxf(mx16[i], mx16[i + 8]);
       const float mx = max3f(max3f(mx16[0], mx16[1], mx16[2]), max3f(mx16[3], mx16[4], mx16[5]), fmaxf(mx16[6], mx16[7]));
-      const float m_cand = fmaxf(m, mx * c);
-      const bool grow = m_cand > m + kRescaleThreshold;
+      // m: the maximum, of scores (E4M3 pages, as in fa_paged_kernel) or of scores in base-2 units
+      const float m_cand = fmaxf(m, kFp8 ? mx : mx * c);
+      const bool grow = kFp8 ? m_cand > m && !((m_cand - m) * c <= pf_growth(true)) : m_cand > m + pf_growth(false);
       const float m_new = grow ? m_cand : m;
-      const float alpha = grow ? ex2_approx(m - m_new) : 1.f;
+      const float alpha = grow ? ex2_approx(kFp8 ? (m - m_new) * c : m - m_new) : 1.f;
       const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      const uint64_t c2 = f2(c, c), nm2 = f2(-m_use, -m_use);
+      const uint64_t c2 = f2(c, c), nm2 = f2(-m_use, -m_use), lift2 = f2(kPfLift, kPfLift);
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       auto exp_chunk = [&](int ch, const uint32_t* cur) {
         uint32_t pk[16];
 #pragma unroll
         for (int jp = 0; jp < 16; ++jp) {
           float x0, x1;
-          f2_split(f2_fma(f2(__uint_as_float(cur[2 * jp]), __uint_as_float(cur[2 * jp + 1])), c2, nm2), x0, x1);
+          const uint64_t s2 = f2(__uint_as_float(cur[2 * jp]), __uint_as_float(cur[2 * jp + 1]));
+          f2_split(kFp8 ? f2_fma(f2_add(s2, nm2), c2, lift2) : f2_fma(s2, c2, nm2), x0, x1);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
           acc[jp & 3] = f2_add(acc[jp & 3], f2(p0, p1));
           pk[jp] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
@@ -593,7 +602,9 @@ __global__ void __launch_bounds__(pf_threads(kFp8), 1)
                             __uint_as_float(r[j + 2]) * inv, __uint_as_float(r[j + 3]) * inv);
         }
       }
-      if (write) p.l_pre[at] = l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994531f;
+      if (write)
+        p.l_pre[at] = l == 0.f ? -INFINITY
+                               : (kFp8 ? m * c + (lg2_approx(l) - kPfLift) : m + lg2_approx(l)) * 0.69314718055994531f;
     }
   }
 

@@ -328,7 +328,8 @@ FA_EXPORT int fa_kv_append(const void* q, const void* k, const void* v, void* q_
  * for tables of more than 2^29 keys a sequence, and for N_q > 2^28.
  *
  * Over bf16 pages P enters P V as bf16; over E4M3 pages the products run on f16 operands: K and V
- * exactly, Q rounded to f16 after clamping to +-65504, P as f16.  NaN stays NaN.  Infinities and NaN
+ * exactly, Q rounded to f16 after clamping to +-65504, P as f16 (weights below 2^-29 of a row's largest, or
+ * 2^-25 in a shared prefix, with fewer bits, and lost below 2^-40, or 2^-36).  NaN stays NaN.  Infinities and NaN
  * in rows of a page that no query row may attend do not reach the result.
  */
 FA_EXPORT size_t fa_paged_workspace_size(int B, int H, int H_kv, int N_q, int d);

@@ -67,3 +67,66 @@ def test_lanes_meet_before_they_read_cleared_rows(exes, tmp_path, fp8):
     o, lse, status = _paged(exes["unordered"], str(tmp_path / "x"), q, k, v, table, lengths, 2, window=window, fp8=fp8)
     assert status == 0
     ref.assert_poisoned(o, lse, want, hit)
+
+
+def sink(gen, gap, n, where, page=16, d=64):
+    """n equal keys and one, with V = 0, whose score lies `gap` above theirs, in E4M3 pages of one head;
+    the key stands first (where = 0) or last.  Returns (q, k, v, numbers, scales, O of the exact result)."""
+    pages = -(-(n + 1) // page)
+    k = torch.zeros(pages, 1, page, d).to(torch.float8_e4m3fn)
+    v = torch.full((pages, 1, page, d), 1.5).to(torch.float8_e4m3fn)
+    at = 0 if where == 0 else n
+    k[at // page, 0, at % page, 0] = 8.0
+    v[at // page, 0, at % page] = 0.0
+    q = torch.zeros(1, 1, 1, d)
+    q[..., 0] = gap           # the score: gap * 8 * k_scale / sqrt(64), with k_scale = 1
+    w = n * np.exp(-float(gap))
+    return q.bfloat16(), k, v, torch.arange(pages, dtype=torch.int32), (1.0, 1.0), 1.5 * w / (1 + w)
+
+
+def assert_sink(o, lse, gap, n, want, lost):
+    """The equal keys' weights are off by half an f16 step, 2^-11 of themselves or `lost` / 2 of the largest
+    weight; scores and exponentials by 2^-16, for the weights and their sum; the result by half a bf16
+    step."""
+    bound = max(2.0 ** -11, lost / 2 * np.exp(float(gap))) + 2 * 2.0 ** -16 + 2.0 ** -8
+    assert (o.double() / want - 1).abs().max() <= bound, (gap, float(o.flatten()[0]), want)
+    assert abs(float(lse) - (gap + np.log1p(n * np.exp(-float(gap))))) <= 2.0 ** -16 + 2.0 ** -20 * gap
+
+
+@pytest.mark.parametrize("where", [0, 1])
+@pytest.mark.parametrize("gap", [14, 18, 22])
+def test_small_weights_over_e4m3_pages(exes, tmp_path, gap, where):
+    """Keys far below the largest score carry the result where the largest key's V is 0."""
+    n = 799
+    q, k, v, table, scales, want = sink(ref.rng(0), gap, n, where)
+    o, lse, status = _paged(exes["late"], str(tmp_path / "x"), q, k, v, table[None], [n + 1], 1, fp8=True, scales=scales)
+    assert status == 0
+    assert_sink(o, lse, gap, n, want, 2.0 ** -39)
+
+
+@pytest.mark.parametrize("where", [0, 1])
+@pytest.mark.parametrize("gap", [14, 18])
+def test_small_weights_over_an_e4m3_prefix(exes, tmp_path, gap, where):
+    n = 450
+    q, k, v, table, scales, want = sink(ref.rng(0), gap, n, where, page=64)
+    o, lse, status = _paged(exes["late"], str(tmp_path / "x"), q, k, v, table[None, :1], [0], 1, fp8=True, scales=scales,
+                            prefix=(table, n + 1, 1, 1))
+    assert status == 0
+    assert_sink(o, lse, gap, n, want, 2.0 ** -35)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_huge_scores_over_e4m3_pages(exes, tmp_path, shared):
+    """Scores of 2^32: the largest weight stays within f16, whatever the rounding of its exponent."""
+    gen = ref.rng(8)
+    k, v, table, _ = ref.make_cache(gen, [100], 1, 16, 64, True, spare=0)
+    q = (torch.randn(1, 3, 1, 64, generator=gen).clamp(-1, 1) * 60000).bfloat16()
+    pages = table[0].contiguous()
+    o, lse, status = _paged(exes["late"], str(tmp_path / "x"), q, k, v, table, [0 if shared else 100], 1, fp8=True,
+                            scales=(6000.0, 0.01), prefix=(pages, 100, 1, 1) if shared else None)
+    assert status == 0 and lse.isfinite().all()
+    keys, values = (torch.from_numpy(ref.sequence(x, pages, 100)[0]) for x in (k, v))
+    s = (q.double()[0, :, 0] @ keys.T) * 6000.0 / 8
+    assert s.amax(1).min() > 2.0 ** 32
+    rows = values[s.argmax(1)] * 0.01
+    assert (o[0, :, 0].double() - rows).abs().max() <= 2.0 ** -7 * 4.48
