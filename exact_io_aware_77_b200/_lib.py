@@ -54,9 +54,13 @@ SIGNATURES = {
     "fa_paged_workspace_size": (_c_size_t, [_c_int] * 5),
     "fa_fwd_paged": (_c_int, [_c_void_p] * 5 + [_c_int] * 5 + [_c_void_p, _c_float, _c_int, _c_int, _c_void_p,
                                                                _c_size_t, _c_void_p]),
+    "fa_fwd_paged_ragged": (_c_int, [_c_void_p] * 6 + [_c_int] * 5 + [_c_void_p, _c_float, _c_int, _c_int, _c_void_p,
+                                                                      _c_size_t, _c_void_p]),
     "fa_shared_workspace_size": (_c_size_t, [_c_int] * 6),
     "fa_fwd_shared": (_c_int, [_c_void_p] * 3 + [_c_int] + [_c_void_p] * 3 + [_c_int] * 5 +
                       [_c_void_p, _c_float, _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    "fa_fwd_shared_ragged": (_c_int, [_c_void_p] * 3 + [_c_int] + [_c_void_p] * 4 + [_c_int] * 5 +
+                             [_c_void_p, _c_float, _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "fa_status_string": (ctypes.c_char_p, [_c_int]),
     "fa_check_status": (_c_int, [_c_void_p]),
     "fa_set_wait_limit_ns": (None, [_c_ull]),
@@ -215,6 +219,13 @@ def fa_fwd_paged(q, cache, lengths, o, lse, B, H, H_kv, N_q, d, strides, scale, 
                  workspace, workspace_bytes, stream)
 
 
+def fa_fwd_paged_ragged(q, cache, lengths, counts, o, lse, B, H, H_kv, N_q, d, strides, scale, causal, window, workspace,
+                        workspace_bytes, stream) -> int:
+    """fa_fwd_paged where only the first counts[b] rows of a sequence are new ones."""
+    return _call("fa_fwd_paged_ragged", q, cache, lengths, counts, o, lse, B, H, H_kv, N_q, d, strides, scale, causal,
+                 window, workspace, workspace_bytes, stream)
+
+
 def fa_shared_workspace_size(B, H, H_kv, N_q, d, prefix_len) -> int:
     return _call("fa_shared_workspace_size", B, H, H_kv, N_q, d, prefix_len)
 
@@ -224,6 +235,13 @@ def fa_fwd_shared(q, cache, prefix_pages, prefix_len, lengths, o, lse, B, H, H_k
     """fa_fwd_paged for a batch whose sequences share their first prefix_len keys."""
     return _call("fa_fwd_shared", q, cache, prefix_pages, prefix_len, lengths, o, lse, B, H, H_kv, N_q, d, strides, scale,
                  causal, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_shared_ragged(q, cache, prefix_pages, prefix_len, lengths, counts, o, lse, B, H, H_kv, N_q, d, strides, scale,
+                         causal, workspace, workspace_bytes, stream) -> int:
+    """fa_fwd_shared where only the first counts[b] rows of a sequence are new ones."""
+    return _call("fa_fwd_shared_ragged", q, cache, prefix_pages, prefix_len, lengths, counts, o, lse, B, H, H_kv, N_q, d,
+                 strides, scale, causal, workspace, workspace_bytes, stream)
 
 
 def fa_status_string(status: int) -> str:

@@ -833,8 +833,8 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* o, 
                     void* stream);
 
 static int paged_impl(const void* q, const fa_paged_kv* cache, const int* prefix_pages, int prefix_len,
-                      const int* lengths, void* o, float* lse, int B, int H, int H_kv, int N_q, int d,
-                      const fa_strides* strides, float scale, int causal, int window, void* workspace,
+                      const int* lengths, const int* counts, void* o, float* lse, int B, int H, int H_kv, int N_q,
+                      int d, const fa_strides* strides, float scale, int causal, int window, void* workspace,
                       size_t workspace_bytes, void* stream);
 
 int fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N, int d,
@@ -1103,8 +1103,15 @@ size_t fa_paged_workspace_size(int B, int H, int H_kv, int N_q, int d) {
 int fa_fwd_paged(const void* q, const fa_paged_kv* cache, const int* lengths, void* o, float* lse, int B, int H,
                  int H_kv, int N_q, int d, const fa_strides* strides, float scale, int causal, int window,
                  void* workspace, size_t workspace_bytes, void* stream) {
+  return fa_fwd_paged_ragged(q, cache, lengths, nullptr, o, lse, B, H, H_kv, N_q, d, strides, scale, causal, window,
+                             workspace, workspace_bytes, stream);
+}
+
+int fa_fwd_paged_ragged(const void* q, const fa_paged_kv* cache, const int* lengths, const int* counts, void* o,
+                        float* lse, int B, int H, int H_kv, int N_q, int d, const fa_strides* strides, float scale,
+                        int causal, int window, void* workspace, size_t workspace_bytes, void* stream) {
   if (!(causal == 0 || causal == 1) || window < 0) return FA_ERR_MASK;
-  return paged_impl(q, cache, nullptr, 0, lengths, o, lse, B, H, H_kv, N_q, d, strides, scale, causal, window,
+  return paged_impl(q, cache, nullptr, 0, lengths, counts, o, lse, B, H, H_kv, N_q, d, strides, scale, causal, window,
                     workspace, workspace_bytes, stream);
 }
 
@@ -1117,17 +1124,25 @@ size_t fa_shared_workspace_size(int B, int H, int H_kv, int N_q, int d, int pref
 int fa_fwd_shared(const void* q, const fa_paged_kv* cache, const int* prefix_pages, int prefix_len, const int* lengths,
                   void* o, float* lse, int B, int H, int H_kv, int N_q, int d, const fa_strides* strides, float scale,
                   int causal, void* workspace, size_t workspace_bytes, void* stream) {
+  return fa_fwd_shared_ragged(q, cache, prefix_pages, prefix_len, lengths, nullptr, o, lse, B, H, H_kv, N_q, d, strides,
+                              scale, causal, workspace, workspace_bytes, stream);
+}
+
+int fa_fwd_shared_ragged(const void* q, const fa_paged_kv* cache, const int* prefix_pages, int prefix_len,
+                         const int* lengths, const int* counts, void* o, float* lse, int B, int H, int H_kv, int N_q,
+                         int d, const fa_strides* strides, float scale, int causal, void* workspace,
+                         size_t workspace_bytes, void* stream) {
   if (prefix_len < 0 || prefix_len > kPgMaxKeys) return FA_ERR_SHAPE;
   if (prefix_len > 0 && !prefix_pages) return FA_ERR_NULL;
   if (!(causal == 0 || causal == 1)) return FA_ERR_MASK;
-  return paged_impl(q, cache, prefix_pages, prefix_len, lengths, o, lse, B, H, H_kv, N_q, d, strides, scale, causal, 0,
+  return paged_impl(q, cache, prefix_pages, prefix_len, lengths, counts, o, lse, B, H, H_kv, N_q, d, strides, scale, causal, 0,
                     workspace, workspace_bytes, stream);
 }
 
 // The paged forward, after the prefix's part when there is one.
 static int paged_impl(const void* q, const fa_paged_kv* cache, const int* prefix_pages, int prefix_len,
-                      const int* lengths, void* o, float* lse, int B, int H, int H_kv, int N_q, int d,
-                      const fa_strides* strides, float scale, int causal, int window, void* workspace,
+                      const int* lengths, const int* counts, void* o, float* lse, int B, int H, int H_kv, int N_q,
+                      int d, const fa_strides* strides, float scale, int causal, int window, void* workspace,
                       size_t workspace_bytes, void* stream) {
   if (!q || !cache || !lengths || !o || !lse) return FA_ERR_NULL;
   int st = check_paged(B, H, H_kv, N_q, d);
@@ -1146,13 +1161,14 @@ static int paged_impl(const void* q, const fa_paged_kv* cache, const int* prefix
   const SharedScratch sc = shared_scratch(total, rows, d, pl);
   const size_t need = prefix_len > 0 ? sc.bytes : paged_scratch(rows, d).bytes;
   if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(lengths, 4) || !aligned(workspace, 16) ||
-      !aligned(prefix_pages, 4))
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(lengths, 4) || !aligned(counts, 4) ||
+      !aligned(workspace, 16) || !aligned(prefix_pages, 4))
     return FA_ERR_ALIGN;
   if ((st = check_device()) != FA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   PagedParams p = paged_params(q, *cache, lengths, o, lse, B, H, H_kv, N_q, d, qs, os, scale, causal, window,
                                workspace);
+  p.counts = counts;
   if (prefix_len > 0) {
     unsigned char* w = static_cast<unsigned char*>(workspace);
     p.o_row = reinterpret_cast<float*>(w + sc.o_row);

@@ -1,9 +1,10 @@
 // Attention of a few new query rows per sequence over a paged key/value cache.
 //
 // Sequence b holds lengths[b] keys (read on the device, so that a captured graph follows a
-// growing cache); key j lies in row j % page_size of page table[b][j / page_size].  Query row i of
-// the N_q new ones stands at position lengths[b] - N_q + i, where the causal and window masks
-// apply.  Rows without an allowed key (an idle slot of the batch has length 0) give O = 0 and
+// growing cache); key j lies in row j % page_size of page table[b][j / page_size].  Of its N_q query
+// rows the first counts[b] are new ones (all, without counts): row i stands at position
+// lengths[b] - counts[b] + i, where the causal and window masks apply.  Rows past the count, which are
+// padding, and rows without an allowed key (an idle slot of the batch has length 0) give O = 0 and
 // L = -inf.
 //
 // One item is one (sequence, K/V head, block of 16 of the head's group * N_q rows); its work is
@@ -109,17 +110,17 @@ inline int pg_warps(int d, bool fp8) {
 struct PgRange {
   int first, steps;   // first step (of kStep keys from key 0) and their number
 };
-// The keys run from the lowest that the first new row may attend (its band starts lowest) to the
-// last key, where the last new row stands.
-__host__ __device__ inline PgRange pg_range(int len, int Nq, int window, int step) {
+// The keys run from the lowest that the first of the `count` new rows may attend (its band starts
+// lowest) to the last key, where the last new row stands.
+__host__ __device__ inline PgRange pg_range(int len, int count, int window, int step) {
   PgRange r;
   int lo = 0;
   if (window > 0) {
-    const long long l = (long long)len - Nq - window + 1;
+    const long long l = (long long)len - count - window + 1;
     lo = l > 0 ? int(l) : 0;
   }
   r.first = lo / step;
-  r.steps = len > 0 ? (len - 1) / step - r.first + 1 : 0;
+  r.steps = len > 0 && count > 0 ? (len - 1) / step - r.first + 1 : 0;
   return r;
 }
 // How the line is cut.  A long line falls into one equal stretch per resident warp, and each stretch
@@ -187,6 +188,7 @@ struct PagedParams {
   const float* l_pre;
   const int* table;         // [B, max_pages], rows table_stride apart
   const int* lengths;       // [B]
+  const int* counts;        // [B] new rows of each sequence, or nullptr: all N_q
   long long table_stride;
   Strides q_st, o_st;
   long long total_rows;     // B * H * N_q
@@ -205,10 +207,15 @@ __device__ __forceinline__ int pg_len(const PagedParams& p, int b) {
   return min(max(p.lengths[b], 0), p.max_pages * p.page_size);
 }
 
+// its new rows
+__device__ __forceinline__ int pg_count(const PagedParams& p, int b) {
+  return p.counts ? min(max(p.counts[b], 0), p.Nq) : p.Nq;
+}
+
 // units of one item row (one item) of sequence b
 template <int kStep>
 __device__ __forceinline__ int pg_units(const PagedParams& p, int b) {
-  return kPgSurcharge + pg_range(pg_len(p, b), p.Nq, p.window, kStep).steps;
+  return kPgSurcharge + pg_range(pg_len(p, b), pg_count(p, b), p.window, kStep).steps;
 }
 __device__ __forceinline__ int pg_warp_sum(int x) {
 #pragma unroll
@@ -229,11 +236,12 @@ template <int kStep>
 struct PgCursor {
   int s;            // start of the current item on the line
   int b, j;         // sequence, item of it (K/V head * row_blocks + row block)
-  int len;
+  int len, count;
   PgRange r;
   __device__ void load(const PagedParams& p) {
     len = pg_len(p, b);
-    r = pg_range(len, p.Nq, p.window, kStep);
+    count = pg_count(p, b);
+    r = pg_range(len, count, p.window, kStep);
   }
   __device__ void next(const PagedParams& p) {
     s += kPgSurcharge + r.steps;
@@ -511,20 +519,24 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
       in_item = true;
       b = cur.b, hkv = cur.j / p.row_blocks;
       row0 = (cur.j - hkv * p.row_blocks) * kDecRows;
-      const int pos0 = cur.len - p.Nq;
+      const int pos0 = cur.len - cur.count;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int r = row0 + g + 8 * hf;
         const __nv_bfloat16* src = nullptr;
-        band_lo[hf] = INT_MIN;   // rows past the end stay unmasked, read zero Q and are never written
+        // rows past the end, and padding, stay unmasked and read zero Q; the former are never written, the
+        // latter as 0
+        band_lo[hf] = INT_MIN;
         band_hi[hf] = INT_MAX;
         hq[hf] = -1;
         if (r < p.rows) {
           const int gh = r / p.Nq;
           qi[hf] = r - gh * p.Nq;
           hq[hf] = hkv * p.group + gh;
-          dec_band(pos0 + qi[hf], cur.len, p.causal, p.window, band_lo[hf], band_hi[hf]);
-          src = p.q + p.q_st.at(b, hq[hf], qi[hf]);
+          if (qi[hf] < cur.count) {
+            dec_band(pos0 + qi[hf], cur.len, p.causal, p.window, band_lo[hf], band_hi[hf]);
+            src = p.q + p.q_st.at(b, hq[hf], qi[hf]);
+          }
         }
         // Q as the A operand of every k-step: columns 2t, 2t + 1 (+ 8), or for E4M3 the permuted
         // 4t .. 4t + 3
@@ -708,6 +720,11 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (hq[hf] < 0) continue;
+      if (qi[hf] >= cur.count) {   // padding
+        l = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j][2 * hf] = acc[j][2 * hf + 1] = 0.f;
+      }
       // a row without keys, or whose every key scored -inf, has l = 0; one with a NaN score is NaN
       float inv = l == 0.f ? 0.f : 1.f / l;
       if constexpr (kFp8) inv *= p.v_scale;
@@ -798,7 +815,8 @@ __global__ void __launch_bounds__(32 * kPgMergeWarps) fa_paged_merge_kernel(cons
   const int c0 = steps > 0 ? cut.of(s + kPgSurcharge) : c_item;
   const int c1 = steps > 0 ? cut.of(s + n - 1) : c_item;
   const bool whole = c0 == c1;
-  const int n_own = whole ? 1 : c1 - c0 + 1, n_src = n_own + p.n_pre;
+  const int n_own = whole ? 1 : c1 - c0 + 1;
+  const int n_src = i < pg_count(p, b) ? n_own + p.n_pre : 0;   // padding joins nothing: O = 0, L = -inf
   if (whole && !p.o_row) return;
   // the prefix's rows of one K/V head: those of all sequences, in order
   const long long pre_row = ((long long)hkv * p.B + b) * p.rows + r;

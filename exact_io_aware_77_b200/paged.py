@@ -3,8 +3,8 @@
 Pages are ``[n_pages, H_kv, page_size, d]`` tensors (any strides with a contiguous last dimension),
 bf16 or E4M3 codes (``torch.float8_e4m3fn`` or ``torch.uint8``; K = k_scale * code).  Row j of
 sequence b is row ``j % page_size`` of page ``page_table[b, j // page_size]``.  ``lengths`` counts the
-keys each sequence holds once the new rows are appended: the same tensor serves the append and
-the attention after it.  Page numbers, lengths and positions are read on the device; one out of
+keys each sequence holds once the new rows are appended, and ``counts`` its new rows where they are
+fewer than the batch has: the same tensors serve the append and the attention after it.  Page numbers, lengths and positions are read on the device; one out of
 range is never followed, and ``check_status`` reports it.
 """
 
@@ -183,13 +183,15 @@ def _outputs(q, shape, device, out, lse, workspace, need):
 
 
 def decode_paged(q, k_pages, v_pages, page_table, lengths, scale: float | None = None, causal: bool = False,
-                 window: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, workspace=None):
+                 window: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, workspace=None,
+                 counts=None):
     """O, L for N_q new query rows of each sequence over a paged cache (decode() with lengths of
     their own).
 
     q: bf16 [B, H, N_q, d]; row i of sequence b stands at position ``lengths[b] - N_q + i``, where
-    the causal and window masks apply.  Rows without an allowed key (length 0, or a causal row
-    before the first key) give O = 0 and L = -inf.  Returns O bf16 [B, H, N_q, d] and L fp32
+    the causal and window masks apply; with ``counts`` int32 [B], as given to the append, at
+    ``lengths[b] - counts[b] + i``, and rows from counts[b] on are padding.  Padding, and rows without
+    an allowed key (length 0, or a causal row before the first key), give O = 0 and L = -inf.  Returns O bf16 [B, H, N_q, d] and L fp32
     [B, H, N_q] (``out`` and ``lse`` if given; out may be q itself).
     """
     shape, device, q_st = _first(q, "q")
@@ -197,8 +199,8 @@ def decode_paged(q, k_pages, v_pages, page_table, lengths, scale: float | None =
     cache, H_kv = _cache(k_pages, v_pages, page_table, B, d, device, k_scale, v_scale)
     out, lse, workspace, out_st = _outputs(q, shape, device, out, lse, workspace,
                                            lambda: paged_workspace_size(B, H, H_kv, N_q, d))
-    _launch("fa_fwd_paged", device, q.data_ptr(), cache, _ints(lengths, "lengths", (B,), device), out.data_ptr(),
-            lse.data_ptr(), B, H, H_kv, N_q, d, _lib.STRIDES2.pack(*q_st, *out_st),
+    _launch("fa_fwd_paged_ragged", device, q.data_ptr(), cache, _ints(lengths, "lengths", (B,), device),
+            0 if counts is None else _ints(counts, "counts", (B,), device), out.data_ptr(), lse.data_ptr(), B, H, H_kv, N_q, d, _lib.STRIDES2.pack(*q_st, *out_st),
             1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
             max(-1, min(int(window), 0x7fffffff)),   # (the library's ints have 32 bits)
             workspace.data_ptr(), workspace.nbytes)
@@ -215,12 +217,13 @@ def shared_workspace_size(B: int, H: int, H_kv: int, N_q: int, d: int, prefix_le
 
 def decode_shared(q, k_pages, v_pages, prefix_pages, prefix_length: int, page_table, lengths,
                   scale: float | None = None, causal: bool = False, k_scale: float = 1.0, v_scale: float = 1.0, out=None,
-                  lse=None, workspace=None):
+                  lse=None, workspace=None, counts=None):
     """decode_paged() for a batch whose sequences all begin with the same ``prefix_length`` keys, which
     lie in ``prefix_pages`` (int32 page numbers): their part is computed once for the whole batch.
 
     ``page_table`` and ``lengths`` describe each sequence's own keys, those after the prefix; every row
-    attends the whole prefix and its own keys (up to itself with causal).  Returns O and L of the
+    attends the whole prefix and its own keys (up to itself with causal).  ``counts`` as in
+    decode_paged().  Returns O and L of the
     prefix and the own keys together.
     """
     shape, device, q_st = _first(q, "q")
@@ -232,7 +235,8 @@ def decode_shared(q, k_pages, v_pages, prefix_pages, prefix_length: int, page_ta
     pages = _ints(prefix_pages, "prefix_pages", prefix_pages.shape, device)
     out, lse, workspace, out_st = _outputs(
         q, shape, device, out, lse, workspace, lambda: shared_workspace_size(B, H, H_kv, N_q, d, prefix_length))
-    _launch("fa_fwd_shared", device, q.data_ptr(), cache, pages, prefix_length, _ints(lengths, "lengths", (B,), device),
+    _launch("fa_fwd_shared_ragged", device, q.data_ptr(), cache, pages, prefix_length,
+            _ints(lengths, "lengths", (B,), device), 0 if counts is None else _ints(counts, "counts", (B,), device),
             out.data_ptr(), lse.data_ptr(), B, H, H_kv, N_q, d, _lib.STRIDES2.pack(*q_st, *out_st),
             1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)), workspace.data_ptr(),
             workspace.nbytes)

@@ -294,7 +294,8 @@ typedef struct fa_rotation {
  *   k, v       bf16 [B, H_kv, N, d].
  *   lengths    device int32 [B]: keys of each sequence AFTER the append.
  *   counts     device int32 [B], 0 to N: rows of each sequence that are new, its first ones
- *              (NULL: all N).  Row i < counts[b] becomes row lengths[b] - counts[b] + i of its
+ *              (NULL: all N; the attention after it then takes the same counts, see
+ *              fa_fwd_paged_ragged).  Row i < counts[b] becomes row lengths[b] - counts[b] + i of its
  *              sequence.  Rows past counts[b], and rows whose place would be negative (an idle
  *              slot with length 0), are padding: nothing of them is written, q_out neither.
  *   rotation   NULL: none; q is then copied to q_out.
@@ -315,8 +316,13 @@ FA_EXPORT int fa_kv_append(const void* q, const void* k, const void* v, void* q_
  * where the causal and window masks apply; a row that no key is allowed for (an idle slot with
  * length 0, a causal row before its sequence's first key) gives O = 0 and L = -inf.
  *
+ * The ragged form follows an append with the same counts: of sequence b's N_q rows the first
+ * counts[b] are new ones, row i at position lengths[b] - counts[b] + i, as fa_kv_append placed it; the
+ * others are padding, whatever they hold, and give O = 0 and L = -inf.
+ *
  *   q, o       bf16 [B, H, N_q, d]; o may be q; lse fp32 [B, H, N_q], packed; lengths device int32 [B], read
  *              as 0 when negative, and as max_pages * page_size (with FA_ERR_INDEX) when longer.
+ *   counts     device int32 [B], 0 to N_q (NULL: all N_q).
  *   strides    NULL for packed arrays, else 2 fa_strides (q, o).
  *   workspace  device memory of at least fa_paged_workspace_size(...) bytes, 16-byte aligned,
  *              owned by the caller; overwritten, and free again once the call's work is done.
@@ -336,6 +342,10 @@ FA_EXPORT size_t fa_paged_workspace_size(int B, int H, int H_kv, int N_q, int d)
 FA_EXPORT int fa_fwd_paged(const void* q, const fa_paged_kv* cache, const int* lengths, void* o, float* lse, int B,
                            int H, int H_kv, int N_q, int d, const fa_strides* strides, float scale, int causal,
                            int window, void* workspace, size_t workspace_bytes, void* stream);
+FA_EXPORT int fa_fwd_paged_ragged(const void* q, const fa_paged_kv* cache, const int* lengths, const int* counts,
+                                  void* o, float* lse, int B, int H, int H_kv, int N_q, int d,
+                                  const fa_strides* strides, float scale, int causal, int window, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * fa_fwd_paged for a batch whose sequences all begin with the same prefix_len keys: their part is
@@ -346,8 +356,9 @@ FA_EXPORT int fa_fwd_paged(const void* q, const fa_paged_kv* cache, const int* l
  *   prefix_pages  device int32, ceil(prefix_len / page_size) page numbers of `cache`.  prefix_len = 0
  *                 (prefix_pages may be NULL) is fa_fwd_paged.
  *   lengths, cache->table   each sequence's OWN keys, those after the prefix.  Row i of sequence b
- *                 stands at position prefix_len + lengths[b] - N_q + i; it attends the whole prefix,
- *                 and its own keys as in fa_fwd_paged (causal or all; there is no window).
+ *                 stands at position prefix_len + lengths[b] - N_q + i (ragged: - counts[b] + i); it
+ *                 attends the whole prefix, and its own keys as in fa_fwd_paged (causal or all; there is
+ *                 no window).
  *   workspace     at least fa_shared_workspace_size(...) bytes.
  *
  * Everything else as for fa_fwd_paged.  Three kernels are enqueued.
@@ -357,6 +368,10 @@ FA_EXPORT int fa_fwd_shared(const void* q, const fa_paged_kv* cache, const int* 
                             const int* lengths, void* o, float* lse, int B, int H, int H_kv, int N_q, int d,
                             const fa_strides* strides, float scale, int causal, void* workspace, size_t workspace_bytes,
                             void* stream);
+FA_EXPORT int fa_fwd_shared_ragged(const void* q, const fa_paged_kv* cache, const int* prefix_pages, int prefix_len,
+                                   const int* lengths, const int* counts, void* o, float* lse, int B, int H, int H_kv,
+                                   int N_q, int d, const fa_strides* strides, float scale, int causal, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 FA_EXPORT const char* fa_status_string(int status);

@@ -118,6 +118,8 @@ static int paged_main(bool shared) {
   auto q = read_all<uint16_t>(prefix + ".q");
   auto k = read_all<unsigned char>(prefix + ".k"), v = read_all<unsigned char>(prefix + ".v");
   auto table = read_all<int>(prefix + ".table"), lengths = read_all<int>(prefix + ".lengths");
+  std::vector<int> counts;   // a file of the ragged calls alone
+  if (std::ifstream(prefix + ".counts")) counts = read_all<int>(prefix + ".counts");
   std::vector<uint16_t> o(q.size(), 0x7fc0);
   std::vector<float> lse(size_t(B) * H * Nq, NAN);
   PagedParams p = {};
@@ -132,6 +134,7 @@ static int paged_main(bool shared) {
   p.table = table.data();
   p.table_stride = max_pages;
   p.lengths = lengths.data();
+  p.counts = counts.empty() ? nullptr : counts.data();
   p.q_st = p.o_st = packed(H, Nq, d);
   p.total_rows = (long long)B * H * Nq;
   p.B = B; p.H = H; p.H_kv = Hkv; p.group = H / Hkv; p.Nq = Nq;
@@ -193,6 +196,7 @@ static int paged_main(bool shared) {
   hideable(v, 0);
   hideable(table, 0);
   hideable(lengths, 0);
+  hideable(counts, 0);
   for (auto* part : {&o_part, &l_part, &o_row, &l_row, &o_pre, &l_pre}) hideable(*part, 0xff);
   if (shared) hideable(pages, 0);
   const PrefixParams* xp = shared ? &x : nullptr;

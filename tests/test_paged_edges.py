@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import paged_ref as ref
-from tests.test_paged_edges_emulated import assert_sink, sink
+from tests.test_paged_edges_emulated import assert_sink, ragged_attention, sink
 from tests.test_paged_parity import _cuda, _i32, fa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +46,74 @@ def test_huge_scores_over_e4m3_pages(fa, d):  # noqa: F811
         assert lse.isfinite().all()
         assert (o.cpu().double()[0, :, 0] - rows).abs().max() <= 2.0 ** -7 * 4.48
     assert fa.check_status() == 0
+
+
+RAGGED = [
+    # lengths after the append, counts, N, H, H_kv, d, page, window, fp8, prefix
+    ([50, 4, 0, 130, 2999], [2, 4, 0, 1, 3], 4, 8, 2, 128, 16, 0, False, 0),
+    ([50, 4, 0, 130, 2999], [2, 4, 0, 1, 3], 4, 8, 2, 128, 48, 0, True, 0),
+    ([50, 7, 3, 130, 2999], [5, 0, 2, 1, 4], 5, 20, 1, 64, 16, 70, False, 0),
+    ([50, 7, 3, 130, 2999], [5, 0, 2, 1, 4], 5, 14, 2, 64, 32, 70, True, 0),
+    ([600, 33], [600, 1], 600, 4, 4, 64, 16, 0, False, 0),               # prompts, one of a single token
+    ([40, 21], [11, 3], 13, 6, 2, 256, 64, 0, False, 0),
+    ([40, 4, 0, 130], [2, 4, 0, 1], 4, 8, 2, 128, 64, 0, False, 700),
+    ([40, 4, 0, 130], [2, 4, 0, 1], 4, 8, 2, 128, 64, 0, True, 700),
+    ([3] * 60, [0, 1, 2] * 20, 2, 28, 4, 64, 16, 0, False, 1300),
+    ([3, 40], [0, 3], 3, 68, 1, 256, 16, 0, True, 500),
+]
+
+
+@pytest.mark.parametrize("case", RAGGED, ids=range(len(RAGGED)))
+def test_append_then_attention_of_a_ragged_batch(fa, case):  # noqa: F811
+    """Padded rows through append_kv(counts) and the attention after it with the same lengths and counts,
+    eager and captured; padding rows give 0 and -inf, whatever they hold."""
+    lengths, counts, N, H, H_kv, d, page, window, fp8, prefix = case
+    gen = ref.rng(90 + N + d)
+    B, need = len(lengths), -(-prefix // page)
+    k_pages, v_pages, table, spare = ref.make_cache(gen, lengths, H_kv, page, d, fp8, spare=need + 1)
+    q, k, v = (torch.randn(B, h, N, d, generator=gen).bfloat16() for h in (H, H_kv, H_kv))
+    angle = torch.rand(3200, d // 2, generator=gen) * 6.3
+    for b, c in enumerate(counts):
+        for x in (q, k, v):
+            x[b, :, c:] = float("nan")
+    scales = dict(k_scale=0.0125, v_scale=0.01) if fp8 else {}
+    kp, vp, tab, pages, n, c = _cuda(k_pages, v_pages, table.clamp(min=0), spare[:need].contiguous(), _i32(lengths), _i32(counts))
+    q, k, v, cos, sin = _cuda(q, k, v, angle.cos(), angle.sin())
+
+    def step():
+        qr = fa.append_kv(k, v, kp, vp, tab, n, counts=c, q=q, q_out=q.clone(), cos=cos, sin=sin, **scales)
+        if prefix:
+            return qr, *fa.decode_shared(qr, kp, vp, pages, prefix, tab, n, causal=True, counts=c, **scales)
+        return qr, *fa.decode_paged(qr, kp, vp, tab, n, causal=True, window=window, counts=c, **scales)
+
+    qr, o, lse = step()
+    assert fa.check_status() == 0
+    want = ragged_attention(qr.cpu(), kp.cpu(), vp.cpu(), table, lengths, counts, d ** -0.5, True, window, *scales.values(),
+                            prefix=(spare[:need].tolist(), prefix) if prefix else None)
+    ref.assert_attention(o, lse, want, case)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    graph.replay()
+    assert torch.equal(out[1], o) and torch.equal(out[2], lse)
+    # without counts every row is a new one, as before
+    full = torch.full_like(c, N)
+    args = (q.nan_to_num(), kp, vp)
+    for more in ({}, dict(counts=full)):
+        got = fa.decode_shared(*args, pages, prefix, tab, n, causal=True, **more, **scales)
+        first = got if not more else first
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    assert fa.check_status() == 0
+
+
+def test_counts_are_checked(fa):  # noqa: F811
+    k = torch.zeros(2, 1, 16, 64, device="cuda", dtype=torch.bfloat16)
+    q = torch.zeros(2, 1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    table, n = _cuda(_i32([[0], [1]]), _i32([3, 4]))
+    for bad in (n.long(), n[:1], n.cpu(), torch.zeros(4, device="cuda", dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError):
+            fa.decode_paged(q, k, k, table, n, counts=bad)
+        with pytest.raises(ValueError):
+            fa.decode_shared(q, k, k, table[0], 10, table, n, counts=bad)

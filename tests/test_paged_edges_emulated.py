@@ -130,3 +130,48 @@ def test_huge_scores_over_e4m3_pages(exes, tmp_path, shared):
     assert s.amax(1).min() > 2.0 ** 32
     rows = values[s.argmax(1)] * 0.01
     assert (o[0, :, 0].double() - rows).abs().max() <= 2.0 ** -7 * 4.48
+
+
+def ragged_attention(q, k, v, table, lengths, counts, *args, **kw):
+    """ref.attention() where sequence b has counts[b] new rows; padding gives O = 0 and L = -inf."""
+    got = None
+    for b, c in enumerate(counts):
+        one = ref.attention(q[b:b + 1, :, :c], k, v, table[b:b + 1], lengths[b:b + 1], *args, **kw)
+        got = got or [np.full((*q.shape[:x.ndim],), -np.inf if i == 1 else 0.0) for i, x in enumerate(one)]
+        for x, y in zip(got, one):
+            x[b, :, :c] = y[0]
+    return got
+
+
+RAGGED = [
+    # lengths, counts, N_q, H, H_kv, page, causal, window, fp8, (prefix, splits, keys form)
+    ([50, 7, 0, 130, 33], [2, 4, 0, 1, 0], 4, 4, 2, 16, True, 0, False, None),
+    ([50, 7, 3, 130, 33], [2, 3, 3, 1, 0], 4, 4, 2, 48, True, 0, True, None),
+    ([50, 7, 0, 130, 33], [2, 4, 0, 1, 3], 4, 12, 2, 16, True, 20, False, None),       # two row blocks
+    ([50, 7, 0, 130, 33], [5, 4, 0, 1, 3], 5, 2, 1, 16, False, 9, True, None),
+    ([50, 7, 0, 130], [2, 4, 0, 1], 4, 2, 1, 16, False, 0, False, None),
+    ([5, 7, 0, 60], [2, 4, 0, 1], 4, 4, 2, 16, True, 0, False, (100, 1, 1)),
+    ([5, 7, 0, 60], [3, 1, 0, 4], 4, 2, 1, 64, True, 0, True, (300, 2, 1)),
+    ([3] * 9, [0, 1, 2] * 3, 2, 20, 1, 16, True, 0, False, (140, 2, 0)),               # 360 rows
+]
+
+
+@pytest.mark.parametrize("case", RAGGED, ids=range(len(RAGGED)))
+def test_ragged_rows(exes, tmp_path, case):
+    """A sequence's first counts[b] rows stand where an append with the same counts put them; what the
+    padding rows hold does not matter."""
+    lengths, counts, N_q, H, H_kv, page, causal, window, fp8, prefix = case
+    gen = ref.rng(61 + N_q + page)
+    need = -(-prefix[0] // page) if prefix else 0
+    k, v, table, spare = ref.make_cache(gen, lengths, H_kv, page, 64, fp8, spare=need + 1)
+    q = torch.randn(len(lengths), H, N_q, 64, generator=gen).bfloat16()
+    scales = (0.0125, 0.01) if fp8 else (1.0, 1.0)
+    pages = spare[:need].contiguous()
+    want = ragged_attention(q, k, v, table, lengths, counts, 0.125, causal, window, *scales,
+                            prefix=(pages.tolist(), prefix[0]) if prefix else None)
+    for b, c in enumerate(counts):
+        q[b, :, c:] = float("nan")
+    o, lse, status = _paged(exes["late"], str(tmp_path / "x"), q, k, v, table, lengths, H_kv, causal, window, fp8, ctas=4,
+                            prefix=(pages, *prefix) if prefix else None, files=dict(counts=np.array(counts, dtype=np.int32)))
+    assert status == 0
+    ref.assert_attention(o, lse, want, case)

@@ -4,7 +4,7 @@ validation must end before any use)."""
 import pytest
 
 from exact_io_aware_77_b200 import _lib
-from tests.test_paged_refusals import _append, _cache, _name, _paged, _shared, lib  # noqa: F401
+from tests.test_paged_refusals import A, _append, _cache, _name, _paged, _shared, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("call", [_paged, _shared], ids=["paged", "shared"])
@@ -23,3 +23,19 @@ def test_scales_past_the_exponentials_base_are_refused(lib, call):  # noqa: F811
 def test_scales_without_an_inverse_are_refused(lib, kw):  # noqa: F811
     """1 / scale past fp32's range: zeros would become NaN codes."""
     assert _name(_append(cache=_cache(fp8=1, **kw))) == "FA_ERR_SCALE"
+
+
+def test_ragged_forwards_refuse_like_the_plain_ones(lib):  # noqa: F811
+    """counts may be left out, and must be aligned; the masks, shapes and scratch are checked as ever."""
+    c, ws = A + 65536, 1 << 40
+
+    def paged(counts, window=0, ws_bytes=ws):
+        return _name(_lib.fa_fwd_paged_ragged(A, _cache(), A, counts, A, A, 2, 8, 4, 1, 128, None, 0.1, 1, window, c, ws_bytes, None))
+
+    def shared(counts, prefix=1000, ws_bytes=ws):
+        return _name(_lib.fa_fwd_shared_ragged(A, _cache(), A, prefix, A, counts, A, A, 2, 8, 4, 1, 128, None, 0.1, 1, c, ws_bytes,
+                                               None))
+    for call in (paged, shared):
+        assert call(A + 2) == "FA_ERR_ALIGN"
+        assert call(A, ws_bytes=100) == "FA_ERR_WORKSPACE"
+    assert paged(A, window=-1) == "FA_ERR_MASK" and shared(A, prefix=-1) == "FA_ERR_SHAPE"
