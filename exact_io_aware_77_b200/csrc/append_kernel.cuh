@@ -76,10 +76,10 @@ __device__ __forceinline__ uint2 app_pack_e4m3(const float* f, float inv) {
   return w;
 }
 
-// The angles of pairs p0 .. p0 + 7 at this row: one load of four where they share an axis.  False,
-// with the status set, when a position lies outside the tables.
+// The angles of pairs p0 .. p0 + 7 of a row at these positions of its axes, which lie within the tables:
+// one load of four where they share an axis.
 template <bool kOneAxis>
-__device__ __forceinline__ bool app_angles(const AppendParams& p, int token, int slot, int p0, float* cs, float* sn) {
+__device__ __forceinline__ void app_angles(const AppendParams& p, const int* pos, int p0, float* cs, float* sn) {
   const int half = p.rot >> 1;
   auto load4 = [&](int pos, int q0) {
     const long long at = (long long)pos * half + q0;
@@ -91,14 +91,8 @@ __device__ __forceinline__ bool app_angles(const AppendParams& p, int token, int
     s[0] = fs.x, s[1] = fs.y, s[2] = fs.z, s[3] = fs.w;
   };
   if constexpr (kOneAxis) {
-    const int pos = p.positions ? p.positions[token] : slot;
-    if (unsigned(pos) >= unsigned(p.n_angles)) {
-      atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
-      return false;
-    }
-    load4(pos, p0);
-    load4(pos, p0 + 4);
-    return true;
+    load4(pos[0], p0);
+    load4(pos[0], p0 + 4);
   } else {
     auto axis_of = [&](int pair) {
       int x = 0;
@@ -107,14 +101,7 @@ __device__ __forceinline__ bool app_angles(const AppendParams& p, int token, int
         if (a < p.axes && pair >= p.edge[a - 1]) x = a;
       return x;
     };
-    bool ok = true;
-    // only the positions of axes that own some of these pairs are read; one out of range stands as 0
-    auto pos_of = [&](int axis) {
-      const int pos = p.positions[(long long)axis * p.tokens + token];
-      const bool in = unsigned(pos) < unsigned(p.n_angles);
-      ok = ok && in;
-      return in ? pos : 0;
-    };
+    auto pos_of = [&](int axis) { return axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3]; };
 #pragma unroll
     for (int g = 0; g < 8; g += 4) {
       const int q0 = p0 + g, first = axis_of(q0);
@@ -129,8 +116,6 @@ __device__ __forceinline__ bool app_angles(const AppendParams& p, int token, int
         }
       }
     }
-    if (!ok) atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
-    return ok;
   }
 }
 
@@ -173,6 +158,14 @@ __global__ void __launch_bounds__(kAppThreads) fa_append_kernel(const AppendPara
       x1[j] = *reinterpret_cast<const uint4*>(src + j * st.h + e1);
     }
 
+  // A row is stored whole or not at all, so every thread of it looks at the positions of all its axes.
+  int pos[kOneAxis ? 1 : kAppMaxAxes];
+#pragma unroll
+  for (int a = 0; a < (kOneAxis ? 1 : kAppMaxAxes); ++a) {
+    pos[a] = 0;
+    if (a < p.axes) pos[a] = p.positions ? p.positions[(long long)a * p.tokens + token] : slot;
+  }
+
   // place of the rows: q_out, or the sequence's page
   Strides to = p.qo_st;
   long long at = to.at(b, h0, i);
@@ -187,8 +180,17 @@ __global__ void __launch_bounds__(kAppThreads) fa_append_kernel(const AppendPara
     at = to.at(page, h0, slot - pg * p.page_size);
   }
 
+  bool in_tables = true;
+#pragma unroll
+  for (int a = 0; a < (kOneAxis ? 1 : kAppMaxAxes); ++a)
+    if (a < p.axes) in_tables = in_tables && unsigned(pos[a]) < unsigned(p.n_angles);
+  if (!in_tables) {
+    atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
+    return;
+  }
+
   float cs[8], sn[8];
-  if (turn && !app_angles<kOneAxis>(p, token, slot, 8 * c, cs, sn)) return;
+  if (turn) app_angles<kOneAxis>(p, pos, 8 * c, cs, sn);
 
   const bool codes = kFp8 && what != 0;
   const float inv = what == 1 ? p.k_inv : p.v_inv;

@@ -254,8 +254,10 @@ FA_EXPORT int fa_fwd_fp8(const void* q8, const void* k8, const void* vt8, float 
  *               1 / k_scale and 1 / v_scale in the append, scale * k_scale * log2(e) in the forwards.
  *
  * Page numbers, lengths and positions live on the device, so that a captured graph follows a growing
- * cache.  One that is out of range is never used as an address: what it would place or turn is not
- * stored, or the page reads as zeros, and fa_check_status reports FA_ERR_INDEX.
+ * cache.  One that is out of range is never used as an address, and fa_check_status reports
+ * FA_ERR_INDEX: a row with a position out of range is not stored, neither its q nor its k and v; a row
+ * whose page is, or whose place lies past the table, leaves its k and v out (its q needs no page); and
+ * the forwards read such a page as zeros.
  */
 typedef struct fa_paged_kv {
   void* k;

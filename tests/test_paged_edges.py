@@ -117,3 +117,29 @@ def test_counts_are_checked(fa):  # noqa: F811
             fa.decode_paged(q, k, k, table, n, counts=bad)
         with pytest.raises(ValueError):
             fa.decode_shared(q, k, k, table[0], 10, table, n, counts=bad)
+
+
+@pytest.mark.parametrize("N", [4, 700])   # one head a thread, and four
+def test_a_row_with_a_bad_position_is_not_stored_at_all(fa, N):  # noqa: F811
+    gen = ref.rng(70 + N)
+    H, H_kv, d, page = 32, 8, 128, 16
+    table = torch.arange(2 * (-(-N // page)), dtype=torch.int32).reshape(2, -1)
+    kp, vp = (torch.full((table.numel(), H_kv, page, d), 3.0, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q, k, v = (torch.randn(2, h, N, d, generator=gen).bfloat16().cuda() for h in (H, H_kv, H_kv))
+    positions = torch.randint(0, 99, (3, 2, N), generator=gen, dtype=torch.int32)
+    bad = [(0, 0, 1), (1, 1, 3), (2, 0, N - 1)]
+    for (a, b, i), x in zip(bad, (99, -1, 1 << 30)):
+        positions[a, b, i] = x
+    angle = torch.rand(99, d // 4, generator=gen).cuda()
+    n, q_out = _i32([N, N]).cuda(), torch.full_like(q, 7.0)
+    fa.append_kv(k, v, kp, vp, table.cuda(), n, q=q, q_out=q_out, cos=angle.cos(), sin=angle.sin(),
+                 positions=positions.cuda(), sections=(8, 12, 12))
+    assert fa.STATUS_NAMES[fa.check_status()] == "FA_ERR_INDEX"
+    missing = torch.zeros(2, N, dtype=torch.bool)
+    for _, b, i in bad:
+        missing[b, i] = True
+    for x, old in ((q_out, 7.0), (kp, 3.0), (vp, 3.0)):
+        rows = x.cpu().transpose(1, 2) if x is q_out else \
+            x.cpu().transpose(1, 2).reshape(2, -1, H_kv, d)[:, :N]
+        assert torch.equal((rows == old).all(-1).all(-1), missing)
+        assert not (rows == old).all(-1)[~missing].any()

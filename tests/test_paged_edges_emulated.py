@@ -175,3 +175,37 @@ def test_ragged_rows(exes, tmp_path, case):
                             prefix=(pages, *prefix) if prefix else None, files=dict(counts=np.array(counts, dtype=np.int32)))
     assert status == 0
     ref.assert_attention(o, lse, want, case)
+
+
+@pytest.mark.parametrize("heads", [1, 4])
+@pytest.mark.parametrize("axes", [1, 3])
+def test_a_row_with_a_bad_position_is_not_stored_at_all(exes, tmp_path, axes, heads):
+    """Not its V, not the part of it that does not turn, not the pairs of its other axes; the other rows are."""
+    gen = ref.rng(70)
+    lengths, N, H, H_kv, d, page, rot, n_angles = [20, 9], 4, 2, 1, 64, 16, 32, 30
+    k_pages, v_pages, table, _ = ref.make_cache(gen, lengths, H_kv, page, d, False)
+    q, k, v = (torch.randn(2, h, N, d, generator=gen).bfloat16() for h in (H, H_kv, H_kv))
+    angle = torch.rand(n_angles, rot // 2, generator=gen)
+    sections = [16] if axes == 1 else [4, 4, 8]
+    positions = torch.randint(0, n_angles, (axes, 2, N), generator=gen, dtype=torch.int32)
+    positions[axes - 1, 0, 1], positions[0, 1, 3] = n_angles, -1
+    pre = str(tmp_path / "x")
+    files = dict(q=q, k=k, v=v, kp=k_pages, vp=v_pages, table=table, lengths=np.array(lengths, dtype=np.int32),
+                 cos=angle.cos(), sin=angle.sin(), positions=positions)
+    status = _run(exes["late"], ["append", 2, H, H_kv, N, d, page, k_pages.shape[0], table.shape[1], rot, n_angles, axes,
+                                 *(sections + [0] * 3)[:4], 0, 0, 1.0, 1.0, heads, 0, 1, *_strides(k_pages),
+                                 *_strides(v_pages)], files, pre)
+    assert status == 4
+    good = positions.clone()
+    good[axes - 1, 0, 1], good[0, 1, 3] = 0, 0
+    out, q_bound, pools, bounds = ref.append(q, k, v, k_pages, v_pages, table, lengths, None, angle.cos(), angle.sin(), good,
+                                             tuple(sections), False, 1.0, 1.0)
+    for b, i in ((0, 1), (1, 3)):   # as they were: q_out's filling, the pages' contents
+        out[b, :, i], slot = np.nan, lengths[b] - N + i
+        for pool, bound, x in zip(pools, bounds, (k_pages, v_pages)):
+            at = int(table[b, slot // page]), slice(None), slot % page
+            pool[at], bound[at] = ref._np(x)[at], 0.0
+    before = torch.full(q.shape, 0x4242, dtype=torch.int16).view(torch.bfloat16)
+    got = [torch.from_numpy(np.fromfile(f"{pre}.{x}", dtype=np.uint8)).view(torch.bfloat16).reshape(k_pages.shape)
+           for x in ("kp", "vp")]
+    ref.assert_append(_bf16(pre + ".q_out", q.shape), *got, (out, q_bound, pools, bounds), before)
