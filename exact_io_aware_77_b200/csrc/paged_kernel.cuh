@@ -297,10 +297,7 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
   const int per = (p.B + 31) >> 5;
   const int sb0 = min(p.B, lane * per), sb1 = min(p.B, sb0 + per);
   int mine = 0;
-  for (int b = sb0; b < sb1; ++b) {
-    mine += pg_units<kStep>(p, b);
-    if (blockIdx.x == 0 && p.lengths[b] > p.max_pages * p.page_size) atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
-  }
+  for (int b = sb0; b < sb1; ++b) mine += pg_units<kStep>(p, b);
   // the next piece's number, asked for ahead of its use (lane 0)
   auto ask = [&] {
     if (lane == 0) {
@@ -804,6 +801,8 @@ __global__ void __launch_bounds__(32 * kPgMergeWarps) fa_paged_merge_kernel(cons
     const int u = pg_units<kStep>(p, x);
     all += u;
     before += x < b ? u : 0;
+    // (reported here, as any CTA of the grid before may be taken over, and then never runs)
+    if (grow == 0 && p.lengths[x] > p.max_pages * p.page_size) atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
   }
   before = pg_warp_sum(before);
   const int total = pg_warp_sum(all) * HR, n = pg_units<kStep>(p, b);

@@ -199,6 +199,9 @@ inline void emu_thread_exit();
 
 // the next CTA to run: a running one may take it over (cta_steal_async)
 inline std::atomic<unsigned> emu_next_cta{0};
+// which CTA goes first (the others follow in order, round to the one before it)
+inline unsigned emu_first_cta = 0;
+inline unsigned emu_cta(unsigned turn) { return (turn + emu_first_cta) % gridDim.x; }
 
 // Runs the grid one CTA after another.  `external_smem` (for kernels that declare their own
 // extern shared array) is refilled with 0xFF before every CTA; otherwise each CTA gets a fresh
@@ -229,7 +232,7 @@ void emu_launch(unsigned grid, unsigned block, size_t smem_bytes, F call, unsign
     for (unsigned tx = 0; tx < block; ++tx)
       th.emplace_back([&, tx] {
         threadIdx.x = tx;
-        blockIdx.x = bx;
+        blockIdx.x = emu_cta(bx);
         g_blk = &ctx;
         call();
         emu_thread_exit();

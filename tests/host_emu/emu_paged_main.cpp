@@ -38,6 +38,8 @@ struct Hidden {
   int fill;
 };
 static bool hide_inputs = false;
+// With "second" there the paged grid's CTA 1 goes first, and CTA 0 last: it may be taken over.
+static unsigned first_cta = 0;
 static std::vector<Hidden> hidden;
 static bool is_hidden = false;
 static std::mutex hidden_mu;
@@ -97,8 +99,10 @@ void run_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& 
                [&] { fa_prefix_kernel<D, kFp8>(q_map(*x, D), pk, pv, *x); }, dec_smem);
   }
   hide();
+  emu_first_cta = first_cta;
   emu_launch(unsigned(p.warps) * pg_parts(D), 32, PgLayout<D, kFp8>::kSmemBytes,
              [&] { fa_paged_kernel<D, kFp8>(tk, tv, p); }, dec_smem);
+  emu_first_cta = 0;
   hide();
   // four warps a row, or one when there are many rows
   emu_launch(unsigned(p.total_rows), p.total_rows <= 48 ? 32 * kPgMergeWarps : 32, pg_merge_smem(D),
@@ -287,7 +291,8 @@ static int append_main() {
 int main(int argc, char** argv) {
   if (argc < 2) return 2;
   hide_inputs = std::string(argv[1]) == "hidden";
-  arg = argv + (hide_inputs ? 3 : 2);
+  first_cta = std::string(argv[1]) == "second";
+  arg = argv + (hide_inputs || first_cta ? 3 : 2);
   if (arg > argv + argc) return 2;
   const std::string what = arg[-1];
   return what == "append" ? append_main() : paged_main(what == "shared");

@@ -357,7 +357,7 @@ inline void queue_answer(uint32_t at, uint32_t bar) {
     BlockCtx* saved = g_blk;
     g_blk = blk;
     const unsigned c = emu_next_cta++;
-    int32_t answer[4] = {c < gridDim.x ? int32_t(c) : -1, 0, 0, 0};
+    int32_t answer[4] = {c < gridDim.x ? int32_t(emu_cta(c)) : -1, 0, 0, 0};
     std::memcpy(smem_at(at, 16), answer, 16);
     bar_complete_tx(bar, 16);
     g_blk = saved;

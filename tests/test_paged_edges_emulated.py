@@ -23,9 +23,10 @@ def exes(tmp_path_factory):
 
 
 def _paged(exe, pre, q, k, v, table, lengths, H_kv, causal=True, window=0, fp8=False, ctas=3, prefix=None, hidden=False,
-           files=(), scales=(0.0125, 0.01)):
+           files=(), scales=(0.0125, 0.01), second=False):
     """Runs the paged kernels, or (prefix = (page numbers, length, splits, keys form)) the shared form's;
-    returns O, L and the status."""
+    returns O, L and the status.  hidden: every grid's inputs appear with its wait; second: the paged
+    grid's second CTA runs first."""
     B, H, N_q, d = q.shape
     ks, vs = scales if fp8 else (1.0, 1.0)
     args = ["shared" if prefix else "paged", B, H, H_kv, N_q, d, k.shape[2], k.shape[0], table.shape[1], causal, window,
@@ -34,7 +35,7 @@ def _paged(exe, pre, q, k, v, table, lengths, H_kv, causal=True, window=0, fp8=F
     if prefix:
         args += list(prefix[1:])
         inputs["pages"] = prefix[0]
-    status = _run(exe, (["hidden"] if hidden else []) + args, inputs, pre)
+    status = _run(exe, (["hidden"] if hidden else ["second"] if second else []) + args, inputs, pre)
     lse = torch.from_numpy(np.fromfile(pre + ".lse", dtype=np.float32)).reshape(B, H, N_q)
     return _bf16(pre + ".o", q.shape), lse, status
 
@@ -209,3 +210,16 @@ def test_a_row_with_a_bad_position_is_not_stored_at_all(exes, tmp_path, axes, he
     got = [torch.from_numpy(np.fromfile(f"{pre}.{x}", dtype=np.uint8)).view(torch.bfloat16).reshape(k_pages.shape)
            for x in ("kp", "vp")]
     ref.assert_append(_bf16(pre + ".q_out", q.shape), *got, (out, q_bound, pools, bounds), before)
+
+
+@pytest.mark.parametrize("ctas", [1, 3])
+def test_too_long_lengths_are_reported_whoever_runs(exes, tmp_path, ctas):
+    """The report does not depend on CTA 0 of the paged grid, whose work another CTA may take over."""
+    gen = ref.rng(6)
+    k, v, table, _ = ref.make_cache(gen, [64, 600], 1, 16, 64, False, width=38)
+    table = table.clamp(min=0)
+    q = torch.randn(2, 1, 1, 64, generator=gen).bfloat16()
+    for lengths, expected in (([64, 600], 0), ([64, 609], 4)):
+        o, lse, status = _paged(exes["late"], str(tmp_path / "x"), q, k, v, table, lengths, 1, ctas=ctas, second=True)
+        assert status == expected
+        ref.assert_attention(o, lse, ref.attention(q, k, v, table, [64, min(lengths[1], 608)], 0.125, True))
