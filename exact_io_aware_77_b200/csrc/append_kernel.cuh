@@ -136,7 +136,9 @@ __global__ void __launch_bounds__(kAppThreads) fa_append_kernel(const AppendPara
   int hg = rest / kChunks;
   const int c = rest % kChunks;
   const int b = token / p.N, i = token - b * p.N;
-  const int count = p.counts ? min(max(p.counts[b], 0), p.N) : p.N;
+  const int said = p.counts ? p.counts[b] : p.N;
+  const int count = min(max(said, 0), p.N);
+  if (said != count) atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
   const int slot = p.lengths[b] - count + i;
   if (i >= count || slot < 0) return;   // padding: the row has no place, nothing of it is written
 

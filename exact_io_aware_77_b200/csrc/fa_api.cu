@@ -1221,7 +1221,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_PHASES: return "phase mask must be a non-empty subset of 1 | 2 | 4";
     case FA_ERR_INTERNAL: return "kernel could not run as built (dynamic shared memory not 1 KB aligned)";
     case FA_ERR_CACHE: return "bad cache description (pages >= 1, page_size a multiple of 16 up to 32768, table rows)";
-    case FA_ERR_INDEX: return "a page number, length or position lay outside its array";
+    case FA_ERR_INDEX: return "a page number, length, count or position was out of range";
     case FA_ERR_ROTATION: return "bad rotation (rot a multiple of 16 up to d, 1 to 4 axes whose sections add up to rot / 2)";
     case FA_ERR_NOALLOC_LIMIT: return "problem needs more than the 64 MiB built-in scratch of fa_bwd_noalloc";
     default: return "unknown status";

@@ -802,7 +802,8 @@ __global__ void __launch_bounds__(32 * kPgMergeWarps) fa_paged_merge_kernel(cons
     all += u;
     before += x < b ? u : 0;
     // (reported here, as any CTA of the grid before may be taken over, and then never runs)
-    if (grow == 0 && p.lengths[x] > p.max_pages * p.page_size) atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
+    if (grow == 0 && (p.lengths[x] > p.max_pages * p.page_size || (p.counts && p.counts[x] != pg_count(p, x))))
+      atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
   }
   before = pg_warp_sum(before);
   const int total = pg_warp_sum(all) * HR, n = pg_units<kStep>(p, b);

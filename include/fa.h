@@ -71,7 +71,7 @@ typedef enum {
   FA_ERR_INTERNAL = 12,  /* a kernel found it could not run as built (reported by fa_check_status) */
   FA_ERR_PHASES = 13,    /* fa_bwd_phases: phase mask outside 1..7 */
   FA_ERR_CACHE = 14,     /* fa_paged_kv: a count < 1, page_size not a multiple of 16 or > 32768, table_stride < max_pages */
-  FA_ERR_INDEX = 15,     /* a page number, length or position lay outside its array (reported by fa_check_status) */
+  FA_ERR_INDEX = 15,     /* a page number, length, count or position was out of range (reported by fa_check_status) */
   FA_ERR_ROTATION = 16   /* fa_rotation: rot, axes or sections out of range */
 } fa_status;
 
@@ -253,11 +253,15 @@ FA_EXPORT int fa_fwd_fp8(const void* q8, const void* k8, const void* vt8, float 
  *   k_scale, v_scale   finite and > 0, and so must be what the kernels form of them in fp32 (FA_ERR_SCALE):
  *               1 / k_scale and 1 / v_scale in the append, scale * k_scale * log2(e) in the forwards.
  *
- * Page numbers, lengths and positions live on the device, so that a captured graph follows a growing
- * cache.  One that is out of range is never used as an address, and fa_check_status reports
- * FA_ERR_INDEX: a row with a position out of range is not stored, neither its q nor its k and v; a row
- * whose page is, or whose place lies past the table, leaves its k and v out (its q needs no page); and
- * the forwards read such a page as zeros.
+ * Page numbers, lengths, counts and positions live on the device, so that a captured graph follows a
+ * growing cache.  One that is out of range is never used as an address, and fa_check_status reports
+ * FA_ERR_INDEX:
+ *   a position     its row is not stored, neither q nor k and v;
+ *   a page number  the append leaves its rows' k and v out (their q needs no page); the forwards read
+ *                  zeros;
+ *   a length past the table's reach   the append leaves k and v out of the rows past it; the forwards
+ *                  read it as the table's reach;
+ *   a count        is read as 0 or N, the nearer of the two.
  */
 typedef struct fa_paged_kv {
   void* k;
@@ -322,8 +326,7 @@ FA_EXPORT int fa_kv_append(const void* q, const void* k, const void* v, void* q_
  * counts[b] are new ones, row i at position lengths[b] - counts[b] + i, as fa_kv_append placed it; the
  * others are padding, whatever they hold, and give O = 0 and L = -inf.
  *
- *   q, o       bf16 [B, H, N_q, d]; o may be q; lse fp32 [B, H, N_q], packed; lengths device int32 [B], read
- *              as 0 when negative, and as max_pages * page_size (with FA_ERR_INDEX) when longer.
+ *   q, o       bf16 [B, H, N_q, d]; o may be q; lse fp32 [B, H, N_q], packed; lengths device int32 [B].
  *   counts     device int32 [B], 0 to N_q (NULL: all N_q).
  *   strides    NULL for packed arrays, else 2 fa_strides (q, o).
  *   workspace  device memory of at least fa_paged_workspace_size(...) bytes, 16-byte aligned,
@@ -382,7 +385,7 @@ FA_EXPORT const char* fa_status_string(int status);
  * Synchronises `stream`, then reads and clears the device status word of the current
  * device.  Returns FA_ERR_INTERNAL if a kernel since the last check refused to run (its
  * dynamic shared memory was not 1 KB aligned), else FA_ERR_TIMEOUT if one gave up on a
- * bounded wait, else FA_ERR_INDEX if a page number, length or position was out of range,
+ * bounded wait, else FA_ERR_INDEX if a page number, length, count or position was out of range,
  * FA_ERR_CUDA if the synchronisation failed, FA_OK otherwise.
  */
 FA_EXPORT int fa_check_status(void* stream);

@@ -143,3 +143,23 @@ def test_a_row_with_a_bad_position_is_not_stored_at_all(fa, N):  # noqa: F811
             x.cpu().transpose(1, 2).reshape(2, -1, H_kv, d)[:, :N]
         assert torch.equal((rows == old).all(-1).all(-1), missing)
         assert not (rows == old).all(-1)[~missing].any()
+
+
+def test_counts_out_of_range_are_reported(fa):  # noqa: F811
+    gen = ref.rng(80)
+    lengths, N = [20, 33], 4
+    k_pages, v_pages, table, _ = ref.make_cache(gen, lengths, 1, 16, 64, False)
+    q, k, v = (torch.randn(2, h, N, 64, generator=gen).bfloat16() for h in (2, 1, 1))
+    for bad in (-1, 5, -(1 << 31), (1 << 31) - 1):
+        taken = [2, min(max(bad, 0), N)]
+        kp, vp = k_pages.cuda(), v_pages.cuda()
+        c, n = _i32([2, bad]).cuda(), _i32(lengths).cuda()
+        q_out = torch.full_like(q, 7.0).cuda()
+        fa.append_kv(*_cuda(k, v), kp, vp, table.cuda(), n, counts=c, q=q.cuda(), q_out=q_out)
+        assert fa.STATUS_NAMES[fa.check_status()] == "FA_ERR_INDEX"
+        ref.assert_append(q_out, kp, vp, ref.append(q, k, v, k_pages, v_pages, table, lengths, taken, None, None, None, (), False,
+                                                    1.0, 1.0), torch.full_like(q, 7.0))
+        o, lse = fa.decode_paged(q.cuda(), kp, vp, table.cuda(), n, causal=True, counts=c)
+        assert fa.STATUS_NAMES[fa.check_status()] == "FA_ERR_INDEX"
+        ref.assert_attention(o, lse, ragged_attention(q, kp.cpu(), vp.cpu(), table, lengths, taken, 0.125, True))
+    assert fa.check_status() == 0

@@ -223,3 +223,27 @@ def test_too_long_lengths_are_reported_whoever_runs(exes, tmp_path, ctas):
         o, lse, status = _paged(exes["late"], str(tmp_path / "x"), q, k, v, table, lengths, 1, ctas=ctas, second=True)
         assert status == expected
         ref.assert_attention(o, lse, ref.attention(q, k, v, table, [64, min(lengths[1], 608)], 0.125, True))
+
+
+@pytest.mark.parametrize("bad", [-1, 5, -(1 << 31), (1 << 31) - 1])
+def test_counts_out_of_range(exes, tmp_path, bad):
+    """A count outside 0 .. N is read as the nearer of the two, and reported, by the append and the attention."""
+    gen = ref.rng(80)
+    lengths, N, counts = [20, 33], 4, [2, bad]
+    taken = [2, min(max(bad, 0), N)]
+    k_pages, v_pages, table, _ = ref.make_cache(gen, lengths, 1, 16, 64, False)
+    q, k, v = (torch.randn(2, h, N, 64, generator=gen).bfloat16() for h in (2, 1, 1))
+    counts = np.array(counts, dtype=np.int32)
+    pre = str(tmp_path / "x")
+    files = dict(q=q, k=k, v=v, kp=k_pages, vp=v_pages, table=table, lengths=np.array(lengths, dtype=np.int32),
+                 cos=torch.ones(1), sin=torch.ones(1), counts=counts)
+    status = _run(exes["late"], ["append", 2, 2, 1, N, 64, 16, k_pages.shape[0], table.shape[1], 0, 1, 0, 0, 0, 0, 0, 0, 0,
+                                 1.0, 1.0, 1, 1, 0, *_strides(k_pages), *_strides(v_pages)], files, pre)
+    assert status == 4
+    want = ref.append(q, k, v, k_pages, v_pages, table, lengths, taken, None, None, None, (), False, 1.0, 1.0)
+    got = [torch.from_numpy(np.fromfile(f"{pre}.{x}", dtype=np.uint8)).view(torch.bfloat16).reshape(k_pages.shape)
+           for x in ("kp", "vp")]
+    ref.assert_append(_bf16(pre + ".q_out", q.shape), *got, want, torch.full(q.shape, 0x4242, dtype=torch.int16).view(torch.bfloat16))
+    o, lse, status = _paged(exes["late"], pre, q, k_pages, v_pages, table, lengths, 1, files=dict(counts=counts))
+    assert status == 4
+    ref.assert_attention(o, lse, ragged_attention(q, k_pages, v_pages, table, lengths, taken, 0.125, True))
