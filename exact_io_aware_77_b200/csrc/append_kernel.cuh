@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kAppThreads) fa_append_kernel(const AppendPara
   const int said = p.counts ? p.counts[b] : p.N;
   const int count = min(max(said, 0), p.N);
   if (said != count) atomicOr(&g_status, FA_DEVICE_BAD_INDEX);
-  const int slot = p.lengths[b] - count + i;
+  const int slot = max(p.lengths[b], 0) - count + i;
   if (i >= count || slot < 0) return;   // padding: the row has no place, nothing of it is written
 
   // q, k or v; its heads h0 .. h0 + n - 1 are this thread's

@@ -262,6 +262,7 @@ FA_EXPORT int fa_fwd_fp8(const void* q8, const void* k8, const void* vt8, float 
  *   a length past the table's reach   the append leaves k and v out of the rows past it; the forwards
  *                  read it as the table's reach;
  *   a count        is read as 0 or N, the nearer of the two.
+ * A negative length is read as 0, an idle slot, and is no error.
  */
 typedef struct fa_paged_kv {
   void* k;

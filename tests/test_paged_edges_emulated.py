@@ -247,3 +247,21 @@ def test_counts_out_of_range(exes, tmp_path, bad):
     o, lse, status = _paged(exes["late"], pre, q, k_pages, v_pages, table, lengths, 1, files=dict(counts=counts))
     assert status == 4
     ref.assert_attention(o, lse, ragged_attention(q, k_pages, v_pages, table, lengths, taken, 0.125, True))
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31)])
+def test_a_negative_length_is_an_idle_slot(exes, tmp_path, length):
+    """Nothing of its rows is stored, whatever the count, and it is no error."""
+    gen = ref.rng(81)
+    k_pages, v_pages, table, _ = ref.make_cache(gen, [20, 20], 1, 16, 64, False)
+    q, k, v = (torch.randn(2, 1, 4, 64, generator=gen).bfloat16() for _ in range(3))
+    pre = str(tmp_path / "x")
+    files = dict(q=q, k=k, v=v, kp=k_pages, vp=v_pages, table=table, lengths=np.array([20, length], dtype=np.int32),
+                 cos=torch.ones(1), sin=torch.ones(1))
+    status = _run(exes["late"], ["append", 2, 1, 1, 4, 64, 16, k_pages.shape[0], table.shape[1], 0, 1, 0, 0, 0, 0, 0, 0, 0,
+                                 1.0, 1.0, 1, 0, 0, *_strides(k_pages), *_strides(v_pages)], files, pre)
+    assert status == 0
+    want = ref.append(q, k, v, k_pages, v_pages, table, [20, 0], None, None, None, None, (), False, 1.0, 1.0)
+    got = [torch.from_numpy(np.fromfile(f"{pre}.{x}", dtype=np.uint8)).view(torch.bfloat16).reshape(k_pages.shape)
+           for x in ("kp", "vp")]
+    ref.assert_append(_bf16(pre + ".q_out", q.shape), *got, want, torch.full(q.shape, 0x4242, dtype=torch.int16).view(torch.bfloat16))
