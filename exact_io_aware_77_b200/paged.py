@@ -1,7 +1,7 @@
 """Paged key/value cache: appending rotated rows, and attention over the pages.
 
 Pages are ``[n_pages, H_kv, page_size, d]`` tensors (any strides with a contiguous last dimension),
-bf16 or E4M3 codes (``torch.float8_e4m3fn`` or ``torch.uint8``; K = k_scale * code).  Row j of
+bf16 or E4M3 codes (``torch.float8_e4m3fn`` or ``torch.uint8``; K = k_scale * code, V = v_scale * code).  Row j of
 sequence b is row ``j % page_size`` of page ``page_table[b, j // page_size]``.  ``lengths`` counts the
 keys each sequence holds once the new rows are appended, and ``counts`` its new rows where they are
 fewer than the batch has: the same tensors serve the append and the attention after it.  Page numbers, lengths and positions are read on the device; one out of
@@ -74,6 +74,8 @@ def _cache(k_pages, v_pages, page_table, B, d, device, k_scale, v_scale):
     fp8 = dtype is not _BF16
     if fp8 and dtype not in _CODES:
         raise ValueError("pages must be bf16 or E4M3 codes (float8_e4m3fn or uint8)")
+    if not fp8 and not k_scale == v_scale == 1.0:
+        raise ValueError("k_scale and v_scale are the scales of E4M3 codes: bf16 pages have none")
     kb, kh, kn, kc = k_pages.stride()
     vb, vh, vn, vc = v_pages.stride()
     if kc != 1 or vc != 1:

@@ -252,6 +252,7 @@ FA_EXPORT int fa_fwd_fp8(const void* q8, const void* k8, const void* vt8, float 
  *   page_size   a multiple of 16, at most 32768.
  *   k_scale, v_scale   finite and > 0, and so must be what the kernels form of them in fp32 (FA_ERR_SCALE):
  *               1 / k_scale and 1 / v_scale in the append, scale * k_scale * log2(e) in the forwards.
+ *               Not read with fp8 = 0.
  *
  * Page numbers, lengths, counts and positions live on the device, so that a captured graph follows a
  * growing cache.  One that is out of range is never used as an address, and fa_check_status reports

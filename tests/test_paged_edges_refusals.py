@@ -2,8 +2,9 @@
 validation must end before any use)."""
 
 import pytest
+import torch
 
-from exact_io_aware_77_b200 import _lib
+from exact_io_aware_77_b200 import _lib, paged
 from tests.test_paged_refusals import A, _append, _cache, _name, _paged, _shared, lib  # noqa: F401
 
 
@@ -39,3 +40,12 @@ def test_ragged_forwards_refuse_like_the_plain_ones(lib):  # noqa: F811
         assert call(A + 2) == "FA_ERR_ALIGN"
         assert call(A, ws_bytes=100) == "FA_ERR_WORKSPACE"
     assert paged(A, window=-1) == "FA_ERR_MASK" and shared(A, prefix=-1) == "FA_ERR_SHAPE"
+
+
+def test_scales_of_bf16_pages_are_refused():
+    """They would be ignored, and a cache read as if it were unscaled."""
+    k, t = torch.empty(5, 4, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32)
+    for scales in ((0.5, 1.0), (1.0, 2.0), (float("nan"), 1.0)):
+        with pytest.raises(ValueError):
+            paged._cache(k, k, t, 2, 64, -1, *scales)
+        paged._cache(k.to(torch.float8_e4m3fn), k.to(torch.float8_e4m3fn), t, 2, 64, -1, *scales)
