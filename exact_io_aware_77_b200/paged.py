@@ -20,6 +20,7 @@ from . import _lib
 
 _BF16, _INT32, _FP32 = torch.bfloat16, torch.int32, torch.float32
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_INT_MAX = 0x7fffffff
 
 # The checks below read each property of a tensor once and compare device numbers: a generation step
 # takes a few microseconds on the GPU, and the host must not take longer.
@@ -58,12 +59,27 @@ def _ints(t, what, shape, device):
     return at
 
 
+def _small(*sizes):
+    """Sizes that the library's ints hold (ctypes would pass the low 32 bits of any other)."""
+    if max(sizes) > _INT_MAX or min(sizes) < -_INT_MAX:
+        raise ValueError(f"size out of range: {sizes}")
+
+
 def _first(t, what):
     """Shape, device number (-1 on the host) and first three strides of the tensor that sets a call's."""
     shape, device, stride = t.shape, t.get_device(), t.stride()
     if len(shape) != 4 or device < 0 or t.dtype is not _BF16 or stride[3] != 1:
         raise ValueError(f"{what} must be a bf16 CUDA tensor of four dimensions with a contiguous last one")
+    _small(*shape)
     return shape, device, stride[:3]
+
+
+def _prefix_length(n, prefix_pages, page_size):
+    n = int(n)
+    if prefix_pages.dim() != 1 or n < 0 or prefix_pages.shape[0] * page_size < n:
+        raise ValueError("prefix_pages must be a 1-D tensor whose pages hold prefix_length keys")
+    _small(n)
+    return n
 
 
 def _cache(k_pages, v_pages, page_table, B, d, device, k_scale, v_scale):
@@ -123,6 +139,7 @@ def append_kv(k, v, k_pages, v_pages, page_table, lengths, counts=None, q=None, 
         if q.dim() != 4:
             raise ValueError("q must be a tensor [B, H, N, d]")
         H = q.shape[1]
+        _small(H)
         q_shape = (B, H, N, d)
         q_st = _rows(q, "q", q_shape, device)
         if q_out is None:
@@ -161,6 +178,7 @@ def append_kv(k, v, k_pages, v_pages, page_table, lengths, counts=None, q=None, 
 
 def paged_workspace_size(B: int, H: int, H_kv: int, N_q: int, d: int) -> int:
     """Bytes of scratch device memory decode_paged() needs, whatever the lengths are."""
+    _small(B, H, H_kv, N_q, d)
     n = _lib.fa_paged_workspace_size(B, H, H_kv, N_q, d)
     if n == 0:
         raise ValueError("invalid shape")
@@ -204,13 +222,14 @@ def decode_paged(q, k_pages, v_pages, page_table, lengths, scale: float | None =
     _launch("fa_fwd_paged_ragged", device, q.data_ptr(), cache, _ints(lengths, "lengths", (B,), device),
             0 if counts is None else _ints(counts, "counts", (B,), device), out.data_ptr(), lse.data_ptr(), B, H, H_kv, N_q, d, _lib.STRIDES2.pack(*q_st, *out_st),
             1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
-            max(-1, min(int(window), 0x7fffffff)),   # (the library's ints have 32 bits)
+            max(-1, min(int(window), _INT_MAX)),   # (the library's ints have 32 bits)
             workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
 def shared_workspace_size(B: int, H: int, H_kv: int, N_q: int, d: int, prefix_length: int) -> int:
     """Bytes of scratch device memory decode_shared() needs, whatever the lengths are."""
+    _small(B, H, H_kv, N_q, d, prefix_length)
     n = _lib.fa_shared_workspace_size(B, H, H_kv, N_q, d, prefix_length)
     if n == 0:
         raise ValueError("invalid shape")
@@ -231,9 +250,7 @@ def decode_shared(q, k_pages, v_pages, prefix_pages, prefix_length: int, page_ta
     shape, device, q_st = _first(q, "q")
     B, H, N_q, d = shape
     cache, H_kv = _cache(k_pages, v_pages, page_table, B, d, device, k_scale, v_scale)
-    prefix_length = int(prefix_length)
-    if prefix_pages.dim() != 1 or prefix_length < 0 or prefix_pages.shape[0] * k_pages.shape[2] < prefix_length:
-        raise ValueError("prefix_pages must be a 1-D tensor whose pages hold prefix_length keys")
+    prefix_length = _prefix_length(prefix_length, prefix_pages, k_pages.shape[2])
     pages = _ints(prefix_pages, "prefix_pages", prefix_pages.shape, device)
     out, lse, workspace, out_st = _outputs(
         q, shape, device, out, lse, workspace, lambda: shared_workspace_size(B, H, H_kv, N_q, d, prefix_length))

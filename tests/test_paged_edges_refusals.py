@@ -49,3 +49,20 @@ def test_scales_of_bf16_pages_are_refused():
         with pytest.raises(ValueError):
             paged._cache(k, k, t, 2, 64, -1, *scales)
         paged._cache(k.to(torch.float8_e4m3fn), k.to(torch.float8_e4m3fn), t, 2, 64, -1, *scales)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """The library takes ints: 2^32 + 1 must not reach it as 1."""
+    for at in range(5):
+        sizes = [2, 8, 4, 1, 128]
+        sizes[at] += 1 << 32
+        for call in (paged.paged_workspace_size, lambda *s: paged.shared_workspace_size(*s, 100)):
+            with pytest.raises(ValueError):
+                call(*sizes)
+    pages = torch.zeros(1, dtype=torch.int32).expand(1 << 18)
+    assert paged._prefix_length(100, pages, 32768) == 100
+    for n in (1 << 32, (1 << 32) + 100, -1, (1 << 33) + 1):
+        with pytest.raises(ValueError):
+            paged._prefix_length(n, pages, 32768)
+    with pytest.raises(ValueError):
+        paged.shared_workspace_size(2, 8, 4, 1, 128, 1 << 32)
