@@ -1023,7 +1023,9 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, const
                  const int* lengths, const int* counts, const fa_rotation* rotation, int B, int H, int H_kv, int N,
                  int d, const fa_strides* strides, void* stream) {
   if (!k || !v || !lengths || (H > 0 && (!q || !q_out))) return FA_ERR_NULL;
-  if (B < 1 || H < 0 || H_kv < 1 || N < 1 || (long long)H + 2ll * H_kv > 1 << 18 || (long long)B * N > 0x7fffffffLL)
+  // (a block's first token, and those it has room for past the last, stay within an int)
+  if (B < 1 || H < 0 || H_kv < 1 || N < 1 || (long long)H + 2ll * H_kv > 1 << 18 ||
+      (long long)B * N > 0x7fffffffLL - kAppThreads)
     return FA_ERR_SHAPE;
   if (d != 64 && d != 128 && d != 256) return FA_ERR_HEADDIM;
   AppendParams p = {};

@@ -66,3 +66,9 @@ def test_sizes_past_32_bits_are_refused():
             paged._prefix_length(n, pages, 32768)
     with pytest.raises(ValueError):
         paged.shared_workspace_size(2, 8, 4, 1, 128, 1 << 32)
+
+
+def test_the_last_tokens_that_a_block_could_index_are_refused(lib):  # noqa: F811
+    """A block of the append has room for up to 64 tokens: indices past the last one must not wrap round."""
+    for n in ((1 << 31) - 1, (1 << 31) - 64):
+        assert _name(_append(B=1, H=0, q=0, q_out=0, H_kv=1, N=n, d=64)) == "FA_ERR_SHAPE"
