@@ -11,8 +11,10 @@
 // kHeads neighbouring heads of q, k or v at a time, so that its angles and addresses serve all of
 // them and the heads' loads are in flight together.  A row's page is looked up by every
 // thread that writes to it: the lookups of a warp hit the same few words.  HBM bounds it: 8192 tokens of
-// 32 + 8 + 8 heads of 128 (206 MB) take 38.5 us, 5.3 TB/s; one token each of eight sequences takes 6 us
-// from a cold start, all latency.
+// 32 + 8 + 8 heads of 128 (206 MB) take 38.7 us, 5.3 TB/s; one token each of eight sequences takes 6 us
+// from a cold start, all latency.  4444 padded rows with three axes into E4M3 pages (68 MB) take 18.3 us: a
+// thread's loads depend on one another four deep (count and length, rows, positions and page, angles), and 80
+// registers leave three CTAs an SM to hide that.
 #pragma once
 
 #include <cstdint>
@@ -23,7 +25,7 @@
 
 namespace fa {
 
-constexpr int FA_DEVICE_BAD_INDEX = 4;   // device status bit: a page, length or position out of range
+constexpr int FA_DEVICE_BAD_INDEX = 4;   // device status bit: a page, length, count or position out of range
 
 constexpr int kAppThreads = 256;
 constexpr int kAppMaxAxes = 4;
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kAppThreads) fa_append_kernel(const AppendPara
   const bool turn = 16 * c < p.rot && what != 2;
   const bool apart = 16 * c < p.rot && !kInter;
   const int e0 = apart ? 8 * c : 16 * c, e1 = apart ? (p.rot >> 1) + 8 * c : 16 * c + 8;
-  uint4 x0[kHeads], x1[kHeads];   // the heads' loads first: they depend on nothing but the row
+  uint4 x0[kHeads], x1[kHeads];   // the heads' loads first: they wait for the padding test alone
 #pragma unroll
   for (int j = 0; j < kHeads; ++j)
     if (j < n) {

@@ -17,7 +17,8 @@
 //   L = M + ln sum_s exp(L_s - M),  O = sum_s exp(L_s - L) O_s   (M = max_s L_s),
 // in the order of the pieces, so the result does not depend on timing.
 //
-// A CTA is one warp, eight of them to an SM, and waits for no other.  It streams its piece through
+// A CTA is one warp, eight of them to an SM (four at d = 256 over bf16 pages, whose ring is twice as
+// large), and waits for no other.  It streams its piece through
 // a private ring of three stages filled by TMA, across item and piece boundaries, so that the next
 // keys are under way while an item is finished.  SMs do not share HBM evenly (with equal pieces the
 // first warp of the 1.07 GB step was done after 130 us and the last after 175), so most of the line
@@ -34,11 +35,19 @@
 // (2c, 2c + 1) of two keys, which two byte permutes sort into the operands of the even and of the
 // odd columns.
 //
-// What it takes (with its merge): 8 sequences of 32768 keys, 8 heads of 128, bf16, 1.07 GB: 180 us, 6.0 TB/s;
-// the copy rate would be 164, the difference is the first loads (5 us), the merge (5 us after the last
-// piece) and the stretches' uneven ends.  64 sequences of 0 to 16384 keys: 90 us, 5.2 TB/s.  E4M3 codes,
-// 514 MB: 104 to 111 us, 4.6 to 4.9 TB/s, where converting the codes and the MMAs (IPC 1.6) bound it.
-// 1000 keys: 14 us, all of it latency.
+// Weights enter P V in 16 bits, as one MMA a block takes them: bf16 over bf16 pages, unbiased and off by half
+// a step at most, so that O is 0.0021 to 0.0024 from the exact result where its own rounding to bf16 is
+// 0.0017; f16 over E4M3 pages (see kPgLift), where nothing of that shows.  More bits would take a second MMA
+// for the weights' low part.  The row sums add the weights in fp32 before that rounding.
+//
+// What it takes (with its merge): 8 sequences of 32768 keys, 8 heads of 128, bf16, 1.07 GB: 181 to 184 us, 5.8 to
+// 5.9 TB/s; the copy rate would be 164, the difference is the first loads (5 us), the merge (5 us after the
+// last piece) and the stretches' uneven ends.  64 sequences of 0 to 16384 keys: 92 us, 5.1 TB/s.  E4M3 codes,
+// 514 MB: 109 to 113 us, 4.6 to 4.7 TB/s.  There the conversions (2.2 cycles of an SMSP) and MMAs (8) of a 4 KB
+// block take some 400 cycles one after the other, which would be 11 TB/s; with the tensor pipe 31 % busy and
+// IPC 1.6, what bounds it is the chain S, maximum, exponentials, P V of two warps an SMSP.
+// 1000 keys: 14 us, all of it latency.  At d = 256 the accumulators and Q do not fit 255 registers: 272 bytes of
+// spill stores and 332 of loads a thread (bf16), 224 and 240 (E4M3); the other forms spill none.
 #pragma once
 
 #include <climits>
@@ -342,8 +351,8 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
   // ---- loads.  The steps of a piece are looked up a batch of 32 blocks at a time, one block a lane.
   // (Everything below has one place in the code, and not one for the start, one for the steady state and
   // one for a change of pieces: a call that finds the instruction cache cold waits for each line of it.
-  // With L2 flushed before each call a 1000-key step takes 16.4 us so and took 18.5, the d = 64 draft 26.6
-  // and 28.7; the 1.07 GB step in a loop takes 180 us and took 178.)
+  // With L2 flushed before each call a 1000-key step took 16.4 us so and 18.5 before, the d = 64 draft 26.6
+  // and 28.7; the 1.07 GB step in a loop 180 us and 178.)
   int piece_now = -1, piece_load = -1;      // the pieces being worked on and being loaded
   int load_x0 = 0, load_x1 = 0;             // the latter's units
   PgCursor<kStep> begun, ahead;             // its first item, and the one that the look-up has come to

@@ -30,12 +30,15 @@
 // per 64 columns loads it; sequences of more than 128 rows are cut anywhere, and the softmax warps
 // gather their Q rows.  (Gathering all Q took 6 to 9 us of a call.)
 // What it takes: 64 sequences of 8 rows a head over 32768 keys of 8 heads (135 MB, 69 GFLOP) 71 us of a
-// call's 96 to 104, the tensor pipe busy 53 % of them.  There the chain S, exponentials, P V of each stream, which
+// call's 101 to 104, the tensor pipe busy 53 % of them.  There the chain S, exponentials, P V of each stream, which
 // the other stream covers in part, bounds it; with few rows the conversion (E4M3) or reading K and V.  S
 // in two buffers at d = 256 brought 60 sequences of 8 rows over 20000 keys from 97 to 79 us.
 // All exponentials run on MUFU, which keeps a partial result's L good to fp32 and NaN scores NaN.  (With a
 // degree-4 polynomial on the FMA pipe for 4, 6 or 8 of every 16 pairs the call took 94.3, 94.3 and 95.4 us
-// instead of 95.8, an E4M3 batch of 32 sequences over 8192 keys 48.9, 47.8 and 49.4 instead of 48.1.)
+// instead of 95.8, an E4M3 batch of 32 sequences over 8192 keys 48.9, 47.8 and 49.4 instead of 48.1, each over
+// the same inputs again and again.)
+// The bf16 forms use 165 registers (d = 256: 104) and spill none; with E4M3 pages 14 warps leave 128 registers a
+// thread, and the d = 64 and 128 forms spill 24 bytes of stores and 48 of loads.
 // Keys past the prefix's end in its last tile get weight 0; their V rows are cleared first, as the
 // page may hold anything there (0 x NaN is NaN).
 #pragma once

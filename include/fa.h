@@ -311,8 +311,9 @@ typedef struct fa_rotation {
  *   d          64, 128 or 256.
  *
  * The rotation runs in fp32; its result is rounded once, to bf16, or to the nearest E4M3 code of
- * value * (1 / scale), values past 448 to 448.  Pages that are not written keep their contents.  Two
- * rows that name the same place of a page leave one of the two there.
+ * value * (1 / scale), values past 448 to 448.  Pages that are not written keep their contents.  Where two
+ * rows name the same place of a page (a page that stands in the tables twice), each run of 8 elements there
+ * may come from either.
  */
 FA_EXPORT int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, const fa_paged_kv* cache,
                            const int* lengths, const int* counts, const fa_rotation* rotation, int B, int H, int H_kv,
@@ -336,9 +337,11 @@ FA_EXPORT int fa_kv_append(const void* q, const void* k, const void* v, void* q_
  *              Calls that may run at the same time need one each.
  *
  * Two kernels are enqueued.  Meant for few rows: every 16 rows of a K/V head (its query heads
- * times N_q) pass over the keys once.  FA_ERR_SHAPE also when B * H_kv * ceil(rows / 16) times the
- * table's keys / 16 comes to 2^31 or more (4096 sequences, 8 heads and a million keys each do),
- * for tables of more than 2^29 keys a sequence, and for N_q > 2^28.
+ * times N_q) pass over the keys once.  FA_ERR_SHAPE also when B * H_kv * ceil(rows / 16) *
+ * (ceil(table's keys / step) + 2) comes to 2^31 or more, whatever the lengths are (step: 16 keys, or 32 at
+ * d = 64 and 64 at d = 64 over E4M3 pages, 32 at d = 128 over E4M3 pages; 4096 sequences with 8 heads and a
+ * table of a million keys each do at d = 128), for tables of more than 2^29 keys a sequence, and for
+ * N_q > 2^28.
  *
  * Over bf16 pages P enters P V as bf16; over E4M3 pages the products run on f16 operands: K and V
  * exactly, Q rounded to f16 after clamping to +-65504, P as f16 (weights below 2^-29 of a row's largest, or
