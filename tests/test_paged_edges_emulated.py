@@ -1,6 +1,8 @@
 """The paged cache kernels' own CUDA source on the CPU (see test_paged_emulated.py), at the edges of
 what their calls may meet."""
 
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -62,6 +64,8 @@ def test_nothing_is_read_before_the_wait(exes, tmp_path, shared, fp8):
 def test_lanes_meet_before_they_read_cleared_rows(exes, tmp_path, fp8):
     """V rows behind the mask are cleared by some lanes and read by others: no data race (a race
     makes the binary's exit status 66)."""
+    if subprocess.run([exes["unordered"]], capture_output=True).returncode != 2:   # its answer to no arguments
+        pytest.skip("ThreadSanitizer does not run here")
     gen = ref.rng(12)
     lengths, N_q, window = [21, 0, 50, 5], 3, 30
     k, v, table, q, want, hit = ref.poisoned(gen, lengths, N_q, window, 16, fp8)
