@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(32, PgLayout<D, kFp8>::kCtasPerSm)
   }
   __syncwarp();
   // This grid may be scheduled while the one before it runs.  Nothing that another grid may have written
-  // (lengths, tables, q, pages) is read before the wait, and the scratch is not written: that a grid
-  // earlier on the stream has ended makes its writes visible only to the grids that waited for it, and
-  // with a shared prefix this one waits for the prefix's.
+  // (lengths, tables, q, pages) is read before the wait, and the scratch is not written: what a grid
+  // earlier on the stream wrote is visible to a grid that has waited for it, or for one that had, and not
+  // already because that one has seen it.  With a shared prefix this grid waits for the prefix's.
   grid_dep_wait();
   // ---- the line of work: every warp adds up the lengths (lane l a run of `per` sequences)
   const int HR = p.H_kv * p.row_blocks;
@@ -801,8 +801,7 @@ __global__ void __launch_bounds__(32 * kPgMergeWarps) fa_paged_merge_kernel(cons
   const int b = bh / p.H, hq = bh - b * p.H;
   const int hkv = hq / p.group, r = (hq - hkv * p.group) * p.Nq + i;
   const int HR = p.H_kv * p.row_blocks;
-  // not even the lengths are read before the wait: the grid before this one has seen them, which
-  // makes them visible to that grid alone
+  // not even the lengths are read before the wait, though the grid before this one has seen them (see there)
   grid_dep_wait();
   // the row's item on the line, from the lengths alone
   int before = 0, all = 0;
